@@ -69,8 +69,10 @@ enum {
   QAT_ERR_WORKSPACE = 6, /* workspace NULL or smaller than the size query returns          */
   QAT_ERR_HIP = 7,       /* a HIP launch failed; qat_last_error() has the HIP message      */
   QAT_ERR_ALIAS = 8,     /* an output overlaps an input or another output                  */
-  QAT_ERR_SCRATCH = 9    /* the problem exceeds the static scratch of the no-allocation
+  QAT_ERR_SCRATCH = 9,   /* the problem exceeds the static scratch of the no-allocation
                             entry point (qat_noalloc_max_weights)                          */
+  QAT_ERR_TYPE = 11      /* a type or mode argument is not one of its values (qat_mx.h,
+                            qat_kv.h)                                                      */
 };
 
 /* Text of a status code (static storage). */

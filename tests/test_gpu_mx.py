@@ -1,0 +1,219 @@
+"""GPU parity of MXFP4 quantisation and product against the fp64 oracle, through the C ABI.
+
+Quantisation is exact arithmetic but for one rounding, so codes, scales and
+values are compared bit for bit. The product's terms are exact in fp32 (each
+factor has at most 3 significant bits and a power of two); with one fp32 ulp
+allowed to each addition of the matrix cores,
+    |Y - ref| <= u |ref| + (1 + u) 2 gamma_k sum |x w| + least,
+u = eps / 2 of the output's type and `least` half its smallest subnormal.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mx_oracle as MX
+from weight_quantization_aware_amd import _lib as Q
+from tests.helpers import check_bound, gamma, say
+
+pytestmark = pytest.mark.gpu
+
+LEAST = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    Q.lib()
+
+
+def host(t):
+    return t.detach().cpu().double().numpy()
+
+
+def quant(x, **kw):
+    rows, cols = x.shape
+    c = torch.full((rows, cols // 2), 0xAB, dtype=torch.uint8, device="cuda")
+    s = torch.full((rows, cols // 32), 0xAB, dtype=torch.uint8, device="cuda")
+    v = torch.full((rows, cols), 7.0, dtype=x.dtype, device="cuda")
+    Q.qat_mx_quant(x, c, s, v)
+    return c, s, v
+
+
+def check_quant(x):
+    c, s, v = quant(x)
+    codes, scales = MX.quantize(host(x))
+    assert np.array_equal(s.cpu().numpy(), scales)
+    assert np.array_equal(c.cpu().numpy(), MX.pack(codes))
+    want, got = MX.values(codes, scales), host(v)
+    assert np.array_equal(got, want, equal_nan=True)
+    fin = ~np.isnan(want)
+    assert np.array_equal(np.signbit(got)[fin], np.signbit(want)[fin])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(1, 32), (3, 96), (17, 4096), (1000, 160), (5, 11008)])
+def test_quant_bit_exact(rows, cols, dtype):
+    say(f"mx quant {rows}x{cols} {dtype}")
+    g = torch.Generator("cuda").manual_seed(rows * cols)
+    x = torch.randn(rows, cols, generator=g, device="cuda")
+    x = x * torch.exp2(torch.randint(-12, 13, (rows, cols // 32, 1), generator=g, device="cuda").float()).expand(
+        rows, cols // 32, 32).reshape(rows, cols)
+    check_quant(x.to(dtype))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("top", [1.0, 1.5, 1.9921875, 3.0])
+def test_quant_every_value_below_a_maximum(dtype, top):
+    # every 16-bit value up to `top` in blocks whose largest magnitude is `top`
+    b = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(dtype)
+    b = b[b.float().abs() <= top]
+    b = torch.cat([b, torch.zeros(-len(b) % 31, dtype=dtype)]).view(-1, 31)
+    x = torch.cat([torch.full((len(b), 1), top, dtype=dtype), b], 1)
+    check_quant(x.cuda())
+
+
+def test_quant_ties_and_extremes_fp32():
+    g = torch.Generator("cuda").manual_seed(3)
+    ties = torch.randint(-64, 65, (512, 64), generator=g, device="cuda").double() / 16
+    e = torch.randint(-149, 120, (512, 1), generator=g, device="cuda").double()
+    x = torch.from_numpy(np.ldexp(ties.cpu().numpy(), e.cpu().numpy().astype(int))).float().cuda()
+    check_quant(x)
+    z = torch.zeros(2, 32, device="cuda")
+    z[1] = -0.0
+    check_quant(z)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_quant_non_finite_blocks(dtype):
+    x = torch.ones(4, 96, dtype=dtype, device="cuda")
+    x[0, 5], x[1, 40], x[2, 95], x[3, 64] = float("inf"), float("nan"), -float("inf"), 2.0
+    check_quant(x)
+    assert quant(x)[1].tolist() == [[255, 125, 125], [125, 255, 125], [125, 125, 255], [125, 125, 126]]
+
+
+def test_quant_strided_rows_and_partial_outputs():
+    base = torch.randn(9, 256, device="cuda").bfloat16()
+    x = base[:, 64:192]
+    c, s, v = quant(x)
+    cc, ss, vv = quant(x.contiguous())
+    assert torch.equal(c, cc) and torch.equal(s, ss) and torch.equal(v, vv)
+    only = torch.empty_like(vv)
+    Q.qat_mx_quant(x, X_hat=only)
+    c2, s2 = torch.empty_like(c), torch.empty_like(s)
+    Q.qat_mx_quant(x, c2, s2)
+    assert torch.equal(only, v) and torch.equal(c2, c) and torch.equal(s2, s)
+    Q.qat_mx_quant(x[:0], c[:0], s[:0])
+
+
+def operand(rows, cols, seed, lo=118, hi=130):
+    g = torch.Generator("cuda").manual_seed(seed)
+    c = torch.randint(0, 256, (rows, cols // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.randint(lo, hi, (rows, cols // 32), generator=g, device="cuda", dtype=torch.uint8)
+    return c, s, MX.values(MX.unpack(c.cpu().numpy()), s.cpu().numpy())
+
+
+def check_y(y, xv, wv):
+    ref, absprod = MX.gemm(xv, wv)
+    u = torch.finfo(y.dtype).eps / 2
+    bound = u * np.abs(ref) + (1 + u) * 2 * gamma(xv.shape[1]) * absprod + LEAST[y.dtype]
+    check_bound("Y", host(y), ref, bound)
+
+
+def gemm(xc, xs, wc, ws, dtype, out=None):
+    M, N, K = xc.shape[0], wc.shape[0], 2 * xc.shape[1]
+    y = torch.full((M, N), 9.0, dtype=dtype, device="cuda") if out is None else out
+    Q.qat_mx_gemm(xc, xs, wc, ws, y, ws=Q.workspace(Q.mx_ws_bytes(M, N, K)))
+    return y
+
+
+GEMM = [
+    # M, out, in
+    (1, 16, 32), (1, 1, 32), (1, 4096, 4096), (2, 33, 64), (3, 100, 96), (1, 250, 11008), (5, 48, 544), (16, 64, 512),
+    (17, 130, 1056), (31, 65, 2080), (33, 512, 128), (64, 300, 4096), (65, 257, 160), (77, 1024, 3584), (128, 128, 256),
+    (129, 255, 288), (200, 511, 4128), (256, 256, 2048), (300, 770, 1568), (512, 1030, 1024), (1000, 129, 8192),
+    (257, 4100, 480),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,N,K", GEMM)
+def test_gemm(M, N, K, dtype):
+    say(f"mx gemm M={M} out={N} in={K} {dtype}")
+    xc, xs, xv = operand(M, K, 1 + M, 120, 126)
+    wc, ws, wv = operand(N, K, 2 + N, 112, 122)
+    check_y(gemm(xc, xs, wc, ws, dtype), xv, wv)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 96), (16, 40, 512), (40, 100, 512), (300, 300, 544)])
+def test_gemm_wide_scales_and_strided_output(M, N, K):
+    # scales from 2^-60 to 2^60: sums span what fp32 holds; Y a slice of wider rows
+    xc, xs, xv = operand(M, K, 5, 67, 187)
+    wc, ws, wv = operand(N, K, 6, 97, 157)
+    base = torch.full((M, N + 13), 5.0, dtype=torch.bfloat16, device="cuda")
+    y = base[:, 8:8 + N]
+    gemm(xc, xs, wc, ws, torch.bfloat16, out=y)
+    check_y(y, xv, wv)
+    assert (base[:, :8] == 5).all() and (base[:, 8 + N:] == 5).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 96), (16, 40, 1024), (40, 100, 512), (300, 300, 512)])
+def test_gemm_nan_scale_stays_in_its_row(M, N, K):
+    xc, xs, xv = operand(M, K, 7, 120, 126)
+    wc, ws, wv = operand(N, K, 8, 120, 126)
+    xs[M // 2, K // 32 - 1] = 255
+    ws[N // 3, 0] = 255
+    y = host(gemm(xc, xs, wc, ws, torch.float16))
+    nan = np.zeros((M, N), bool)
+    nan[M // 2] = True
+    nan[:, N // 3] = True
+    assert np.array_equal(np.isnan(y), nan)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (1, 100, 96), (2, 33, 544), (7, 257, 2080), (16, 512, 11008),
+                                   (17, 48, 64), (40, 96, 4128), (300, 260, 512)])
+def test_linear_is_quant_and_gemm(M, N, K, dtype):
+    say(f"mx linear M={M} out={N} in={K} {dtype}")
+    g = torch.Generator("cuda").manual_seed(M)
+    x = (torch.randn(M, K + 32, generator=g, device="cuda") * 3).to(dtype)[:, 8:8 + K]
+    wc, ws, wv = operand(N, K, 9, 112, 122)
+    y = torch.full((M, N), 9.0, dtype=dtype, device="cuda")
+    Q.qat_mx_linear(x, wc, ws, y, ws=Q.workspace(Q.mx_ws_bytes(M, N, K)))
+    c, s, v = quant(x)
+    assert torch.equal(y, gemm(c, s, wc, ws, dtype))
+    check_y(y, host(v), wv)
+
+
+def test_linear_of_a_block_with_an_infinity():
+    x = torch.ones(3, 64, dtype=torch.bfloat16, device="cuda")
+    x[1, 40] = float("inf")
+    wc, ws, _ = operand(20, 64, 4, 120, 126)
+    y = torch.zeros(3, 20, dtype=torch.bfloat16, device="cuda")
+    Q.qat_mx_linear(x, wc, ws, y, ws=Q.workspace(Q.mx_ws_bytes(3, 20, 64)))
+    assert torch.isnan(y[1]).all() and torch.isfinite(y[::2]).all()
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_other_stream_and_replayed_graph(M):
+    N, K = 300, 1056
+    wc, ws, wv = operand(N, K, 10, 112, 122)
+    work = Q.workspace(Q.mx_ws_bytes(M, N, K))
+    x = torch.randn(M, K, device="cuda").half()
+    y, want = torch.empty(M, N, dtype=torch.float16, device="cuda"), torch.empty(M, N, dtype=torch.float16, device="cuda")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        Q.qat_mx_linear(x, wc, ws, y, ws=work)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            Q.qat_mx_linear(x, wc, ws, y, ws=work)
+    torch.cuda.current_stream().wait_stream(st)
+    for i in range(4):
+        x.copy_(torch.randn(M, K, device="cuda"))
+        Q.qat_mx_linear(x, wc, ws, want, ws=work)       # eager, on the same workspace, in turn
+        y.fill_(5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), i
+    check_y(y, host(quant(x)[2]), wv)

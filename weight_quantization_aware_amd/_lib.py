@@ -7,6 +7,7 @@ not built, importing the functions raises; there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -90,6 +91,26 @@ _SIGS.update({
                           ctypes.POINTER(BlockAdamW), _c_vp, _c_vp, _c_vp, _c_sz, _c_vp],
 })
 _RES["qat_block_ws_bytes"] = _c_sz
+
+# include/qat_mx.h, include/qat_kv.h
+_SIGS.update({
+    "qat_mx_quant": [_c_vp, _c_i32, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp],
+    "qat_mx_ws_bytes": [_c_i64, _c_i64, _c_i64],
+    "qat_mx_gemm": [_c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i32, _c_vp, _c_i64, _c_vp, _c_sz, _c_vp],
+    "qat_mx_linear": [_c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i32, _c_vp, _c_i64, _c_vp, _c_sz,
+                      _c_vp],
+    "qat_rope_inv_freq": [_c_i32, ctypes.c_double, _c_i32, ctypes.c_double, _c_i64, ctypes.c_double, ctypes.c_double,
+                          _c_vp, _c_vp],
+    "qat_rope": [_c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, ctypes.c_float,
+                 _c_i32, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp],
+    "qat_kv_append": [_c_vp, _c_vp, _c_i32, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i32,
+                      _c_i32, _c_i32, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp],
+    "qat_kv_attn_ws_bytes": [_c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_i64, _c_i64],
+    "qat_kv_attn": [_c_vp, _c_i32, _c_i64, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_i32,
+                    _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, ctypes.c_float, _c_i32, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp,
+                    _c_sz, _c_vp],
+})
+_RES.update({"qat_mx_ws_bytes": _c_sz, "qat_kv_attn_ws_bytes": _c_sz})
 
 _lib = None
 
@@ -412,6 +433,194 @@ def qat_deploy_gemv(X, Wq, s16, zq, bits, Y, group: int = GROUP) -> None:
             a.t("Y", Y, F16, (M, out)))
     a.done()
     _call(fn, *args, _stream())
+
+
+# ---------------------------------------------------------------------------
+# MXFP4 (include/qat_mx.h), rotary positions and the 8-bit cache
+# (include/qat_kv.h). Activations may be slices: rows of any stride over
+# contiguous trailing dimensions. A call runs on its tensors' device, on that
+# device's current stream.
+# ---------------------------------------------------------------------------
+
+_DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+X16 = (torch.bfloat16, torch.float16)
+FP8 = (torch.float8_e4m3fn, torch.uint8)
+E8M0 = (torch.uint8, torch.float8_e8m0fnu)
+I32 = (torch.int32,)
+
+
+class _RowArgs(_Args):
+    """_Args with row-strided activations and a launch on the tensors' device."""
+
+    def rows(self, name: str, t, dtypes, shape):
+        """(pointer, elements between rows) of a tensor [rows, ...] whose trailing dimensions are contiguous."""
+        if t is None:
+            raise ValueError(f"{self.fn}: {name} is required")
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{self.fn}: {name} must be a torch.Tensor, got {type(t).__name__}")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{self.fn}: {name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{self.fn}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        self.seen.append((name, t))
+        row = math.prod(shape[1:])
+        if t.is_contiguous():
+            return t.data_ptr(), max(row, 1)
+        want = 1
+        for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+            if size != 1 and stride != want:
+                raise ValueError(f"{self.fn}: {name} must be contiguous behind its first dimension")
+            want *= size
+        ld = t.stride(0) if shape[0] > 1 else max(row, 1)
+        if ld < row:
+            raise ValueError(f"{self.fn}: {name}'s rows overlap")
+        return t.data_ptr(), ld
+
+    def call(self, *args) -> None:
+        self.done()
+        dev = self.seen[0][1].device
+        if dev.index == torch.cuda.current_device():
+            _call(self.fn, *args, torch.cuda.current_stream(dev).cuda_stream)
+        else:
+            with torch.cuda.device(dev):
+                _call(self.fn, *args, torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _dims(fn: str, name: str, t, n: int, what: str):
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise ValueError(f"{fn}: {name} must be a {n}-D tensor ({what})")
+    return t.shape
+
+
+def qat_mx_quant(X, codes=None, scales=None, X_hat=None) -> None:
+    """MXFP4 codes [rows, cols / 2], scales [rows, cols / 32] (uint8) and values (X's type) of X [rows, cols]."""
+    fn = "qat_mx_quant"
+    rows, cols = _dims(fn, "X", X, 2, "[rows, cols]")
+    a = _RowArgs(fn)
+    p, ld = a.rows("X", X, tuple(_DTYPE_CODE), (rows, cols))
+    if cols % 32:
+        raise ValueError(f"{fn}: X must have a multiple of 32 columns, got {cols}")
+    a.call(p, _DTYPE_CODE[X.dtype], rows, cols, ld, a.t("codes", codes, U8, (rows, cols // 2), optional=True),
+           a.t("scales", scales, E8M0, (rows, cols // 32), optional=True),
+           a.t("X_hat", X_hat, (X.dtype,), (rows, cols), optional=True))
+
+
+def mx_ws_bytes(M: int, out: int, inp: int) -> int:
+    return int(lib().qat_mx_ws_bytes(M, out, inp))
+
+
+def _mx_weight(a: _Args, fn: str, W_codes, W_scales, inp: int):
+    out = _dims(fn, "W_codes", W_codes, 2, "[out, in / 2]")[0]
+    if inp % 32:
+        raise ValueError(f"{fn}: in = {inp} must be a multiple of 32")
+    return (a.t("W_codes", W_codes, U8, (out, inp // 2)), a.t("W_scales", W_scales, E8M0, (out, inp // 32))), out
+
+
+def qat_mx_gemm(X_codes, X_scales, W_codes, W_scales, Y, ws=None) -> None:
+    """Y [M, out] (bf16 or fp16) = X_hat W_hat^T of MXFP4 operands."""
+    fn = "qat_mx_gemm"
+    M, half = _dims(fn, "X_codes", X_codes, 2, "[M, in / 2]")
+    inp = 2 * half
+    a = _RowArgs(fn)
+    w, out = _mx_weight(a, fn, W_codes, W_scales, inp)
+    x = a.t("X_codes", X_codes, U8), a.t("X_scales", X_scales, E8M0, (M, inp // 32))
+    y, ldy = a.rows("Y", Y, X16, (M, out))
+    a.call(*x, *w, M, out, inp, _DTYPE_CODE[Y.dtype], y, ldy, *_ws_opt(a, ws))
+
+
+def _ws_opt(a: _Args, ws):
+    """A workspace of any size, or none: the library says where it is too small."""
+    if ws is None:
+        return None, 0
+    return a.t("ws", ws, None), ws.numel() * ws.element_size()
+
+
+def qat_mx_linear(X, W_codes, W_scales, Y, ws=None) -> None:
+    """Y [M, out] = X_hat W_hat^T with X [M, in] (Y's type) quantised to MXFP4 in the call."""
+    fn = "qat_mx_linear"
+    M, inp = _dims(fn, "X", X, 2, "[M, in]")
+    a = _RowArgs(fn)
+    w, out = _mx_weight(a, fn, W_codes, W_scales, inp)
+    x, ldx = a.rows("X", X, X16, (M, inp))
+    y, ldy = a.rows("Y", Y, (X.dtype,), (M, out))
+    a.call(x, ldx, *w, M, out, inp, _DTYPE_CODE[X.dtype], y, ldy, *_ws_opt(a, ws))
+
+
+ROPE_SCALING = {"plain": 0, "linear": 1, "parts": 2}
+
+
+def rope_inv_freq(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0, original: int = 1,
+                  beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(inv_freq [rot / 2] fp32 on the host, mscale) of a rotary embedding."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"rope_inv_freq: scaling must be one of {sorted(ROPE_SCALING)}, got {scaling!r}")
+    f = torch.empty(max(rot, 2) // 2, dtype=torch.float32)
+    m = ctypes.c_float()
+    _call("qat_rope_inv_freq", rot, base, ROPE_SCALING[scaling], factor, original, beta_fast, beta_slow, f.data_ptr(),
+          ctypes.addressof(m))
+    return f, float(m.value)
+
+
+def qat_rope(q, pos, inv_freq, q_out, k=None, k_out=None, half: bool = True, mscale: float = 1.0,
+             inverse: bool = False) -> None:
+    """Rotary positions of q [tokens, heads, head_dim] and k; an output may be its own input."""
+    fn = "qat_rope"
+    T, hq, d = _dims(fn, "q", q, 3, "[tokens, heads, head_dim]")
+    a = _RowArgs(fn)
+    qp, ldq = a.rows("q", q, X16, (T, hq, d))
+    qo, ldqo = a.rows("q_out", q_out, (q.dtype,), (T, hq, d))
+    hk, kp, ldk, ko, ldko = 0, None, 0, None, 0
+    if k is not None or k_out is not None:
+        hk = _dims(fn, "k", k, 3, "[tokens, heads, head_dim]")[1]
+        kp, ldk = a.rows("k", k, (q.dtype,), (T, hk, d))
+        ko, ldko = a.rows("k_out", k_out, (q.dtype,), (T, hk, d))
+    n = _dims(fn, "inv_freq", inv_freq, 1, "[rot / 2]")[0]
+    a.call(qp, kp, a.t("pos", pos, I32, (T,)), a.t("inv_freq", inv_freq, F32), T, hq, hk, d, 2 * n, int(half),
+           int(inverse), mscale, _DTYPE_CODE[q.dtype], ldq, ldk, qo, ldqo, ko, ldko)
+
+
+def _kv_cache(a: _Args, fn: str, heads: int, d: int, cu, lens, table, k_cache, v_cache, k_scale, v_scale):
+    """Pointers and sizes that qat_kv_append and qat_kv_attn share."""
+    n, _, page, _ = _dims(fn, "k_cache", k_cache, 4, "[pages, heads, page, head_dim]")
+    B, cols = _dims(fn, "table", table, 2, "[batch, pages of a sequence]")
+    ptrs = (a.t("cu", cu, I32, (B + 1,)), a.t("lens", lens, I32, (B,)), a.t("table", table, I32), cols)
+    cache = (a.t("k_cache", k_cache, FP8, (n, heads, page, d)), a.t("v_cache", v_cache, FP8, (n, heads, d, page)),
+             a.t("k_scale", k_scale, F32, (n, heads)), a.t("v_scale", v_scale, F32, (n, heads)))
+    return ptrs, cache, B, page, n
+
+
+def qat_kv_append(k, v, cu, lens, table, k_cache, v_cache, k_scale, v_scale, max_new: Optional[int] = None) -> None:
+    """New keys and values [tokens, heads, head_dim] into the cache; max_new: a bound on a sequence's new tokens."""
+    fn = "qat_kv_append"
+    T, h, d = _dims(fn, "k", k, 3, "[tokens, heads, head_dim]")
+    a = _RowArgs(fn)
+    kp, ldk = a.rows("k", k, X16, (T, h, d))
+    vp, ldv = a.rows("v", v, (k.dtype,), (T, h, d))
+    ptrs, cache, B, page, n = _kv_cache(a, fn, h, d, cu, lens, table, k_cache, v_cache, k_scale, v_scale)
+    a.call(kp, vp, _DTYPE_CODE[k.dtype], ldk, ldv, *ptrs, T, B, h, d, page, n, T if max_new is None else max_new,
+           *cache)
+
+
+def kv_attn_ws_bytes(tokens: int, batch: int, heads_q: int, heads_kv: int, head_dim: int, max_new: int,
+                     max_len: int) -> int:
+    return int(lib().qat_kv_attn_ws_bytes(tokens, batch, heads_q, heads_kv, head_dim, max_new, max_len))
+
+
+def qat_kv_attn(q, cu, lens, table, k_cache, v_cache, k_scale, v_scale, out, softmax_scale: float,
+                causal: bool = True, max_new: Optional[int] = None, max_len: Optional[int] = None, ws=None) -> None:
+    """out [tokens, heads, head_dim] = attention of q over the cache; max_new, max_len: bounds on a sequence's new
+    tokens and on its length."""
+    fn = "qat_kv_attn"
+    T, hq, d = _dims(fn, "q", q, 3, "[tokens, heads, head_dim]")
+    hk = _dims(fn, "k_cache", k_cache, 4, "[pages, heads, page, head_dim]")[1]
+    a = _RowArgs(fn)
+    qp, ldq = a.rows("q", q, X16, (T, hq, d))
+    ptrs, cache, B, page, n = _kv_cache(a, fn, hk, d, cu, lens, table, k_cache, v_cache, k_scale, v_scale)
+    op, ldo = a.rows("out", out, (q.dtype,), (T, hq, d))
+    if max_len is None:
+        max_len = ptrs[3] * page
+    a.call(qp, _DTYPE_CODE[q.dtype], ldq, *ptrs, T, B, hq, hk, d, page, n, *cache, softmax_scale, int(causal),
+           T if max_new is None else max_new, max_len, op, ldo, *_ws_opt(a, ws))
 
 
 # ---------------------------------------------------------------------------

@@ -111,6 +111,7 @@ QAT_API const char* qat_status_string(int32_t st) {
     case QAT_ERR_HIP: return "HIP launch failed (see qat_last_error)";
     case QAT_ERR_ALIAS: return "an output overlaps an input or another output";
     case QAT_ERR_SCRATCH: return "out * in exceeds the static scratch of the no-allocation entry point (qat_noalloc_max_weights)";
+    case QAT_ERR_TYPE: return "a type or mode argument is not one of its values";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,353 @@
+// Microscaled 4-bit floating point (MXFP4): quantisation and the product on
+// the block-scaled matrix instructions (gfx950, wave64).
+//
+// Format: 32 consecutive elements of a row share the scale 2^e (byte e + 127);
+// elements are E2M1 codes, two to a byte, the even element in the low half.
+#include <string.h>
+
+#include "../../include/qat_mx.h"
+#include "qat_check.h"
+#include "qat_device.h"
+#include "qat_internal.h"
+
+namespace qat {
+namespace {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4v __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// ---------------------------------------------------------------------------
+// Quantisation. A thread owns 8 consecutive elements, four lanes a block: the
+// block's largest magnitude is the largest of the elements' fp32 bits without
+// the sign (integers order like magnitudes, and infinities and NaN come out on
+// top), joined over the four lanes by two DPP exchanges. x 2^-e is exact, so
+// the only rounding is the conversion's own. One pass over X; bound by HBM.
+// ---------------------------------------------------------------------------
+template <int DT>
+__device__ __forceinline__ void load8(const void* p, int64_t i, float (&x)[8]) {
+  if constexpr (DT == QAT_F32) {
+    const f32x4 a = *(const f32x4*)((const float*)p + i), b = *(const f32x4*)((const float*)p + i + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[j] = a[j];
+      x[j + 4] = b[j];
+    }
+  } else if constexpr (DT == QAT_BF16) {
+    const uint4 v = *(const uint4*)((const uint16_t*)p + i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = __builtin_bit_cast(float, w[j] << 16);
+      x[2 * j + 1] = __builtin_bit_cast(float, w[j] & 0xFFFF0000u);
+    }
+  } else {
+    typedef _Float16 f16x8_ __attribute__((ext_vector_type(8)));
+    const f16x8_ v = *(const f16x8_*)((const _Float16*)p + i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = (float)v[j];
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
+  if (dtype == QAT_BF16) return pack_bf16x2(a, b);
+  return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(void* p, int64_t i, const float (&x)[8]) {
+  if constexpr (DT == QAT_F32) {
+    *(f32x4*)((float*)p + i) = f32x4{x[0], x[1], x[2], x[3]};
+    *(f32x4*)((float*)p + i + 4) = f32x4{x[4], x[5], x[6], x[7]};
+  } else {
+    *(uint4*)((uint16_t*)p + i) = make_uint4(pack2(x[0], x[1], DT), pack2(x[2], x[3], DT), pack2(x[4], x[5], DT),
+                                             pack2(x[6], x[7], DT));
+  }
+}
+
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kCtrl, 0xF, 0xF, false);
+}
+
+// The lane's 8 codes (a dword) and its block's scale byte; every lane of the
+// block's four calls it together.
+__device__ __forceinline__ uint32_t quant8(const float (&x)[8], uint32_t& byte) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) a = max(a, __builtin_bit_cast(uint32_t, x[j]) & 0x7FFFFFFFu);
+  a = max(a, dpp_u32<kDppXor1>(a));
+  a = max(a, dpp_u32<kDppXor2>(a));
+  const bool odd = a >= 0x7F800000u;
+  const uint32_t ex = a >> 23;
+  byte = odd ? 255u : (ex > 2 ? ex - 2 : 0u);
+  // 2^-e = 2^(127 - byte), a normal number for every byte up to 252
+  const float inv = __builtin_bit_cast(float, odd ? 0u : (254u - byte) << 23);
+  uint32_t c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[0] * inv, x[1] * inv, 1.0f, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[2] * inv, x[3] * inv, 1.0f, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[4] * inv, x[5] * inv, 1.0f, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[6] * inv, x[7] * inv, 1.0f, 3);
+  return odd ? 0u : c;
+}
+
+struct QuantArgs {
+  const void* X;
+  int64_t ldx;
+  uint32_t chunks;      // rows * cols / 8, below 2^31
+  uint32_t row_chunks;  // cols / 8
+  FastDiv div;          // by row_chunks
+  uint8_t* codes;
+  uint8_t* scales;
+  void* x_hat;
+};
+
+template <int DT>
+__global__ __launch_bounds__(256) void k_mx_quant(const QuantArgs a) {
+  // chunks is a multiple of 4, so the four lanes of a block are all in or out
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= a.chunks) return;
+  const uint32_t row = a.div.div(i), col = (i - row * a.row_chunks) * 8;
+  float x[8];
+  load8<DT>(a.X, (int64_t)row * a.ldx + col, x);
+  uint32_t byte;
+  const uint32_t c = quant8(x, byte);
+  if (a.codes) {
+    *(uint32_t*)(a.codes + (int64_t)i * 4) = c;
+    if ((i & 3) == 0) a.scales[i >> 2] = (uint8_t)byte;
+  }
+  if (a.x_hat) {
+    // 2^e; the byte 0 is 2^-127, a subnormal, and 255 an infinity that makes
+    // NaN of the zero codes
+    const float s = __builtin_bit_cast(float, byte ? byte << 23 : 0x00400000u);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f32x2 p;
+      if (j == 0) p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0);
+      else if (j == 1) p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
+      else if (j == 2) p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2);
+      else p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
+      v[2 * j] = p[0] * s;
+      v[2 * j + 1] = p[1] * s;
+    }
+    store8<DT>(a.x_hat, (int64_t)i * 8, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Product, v_mfma_scale_f32_16x16x128_f8f6f4 with both operands E2M1: lane l
+// holds 32 consecutive elements (16 bytes) of row l & 15 and their scale.
+// The contraction's order is free as long as both operands share it: over 512
+// elements (16 blocks) lane group g = l >> 4 takes block 4 g + j in step j, so
+// a lane reads 64 consecutive bytes of its row and its four scales are one
+// dword, whose byte j the instruction selects.
+// ---------------------------------------------------------------------------
+struct Piece {
+  i32x4v c[4];
+  uint32_t s;
+};
+
+struct ProductArgs {
+  const uint8_t* xc;
+  const uint8_t* xs;
+  const uint8_t* wc;
+  const uint8_t* ws;
+  int M, N, K;
+  void* Y;
+  int64_t ldy;
+};
+
+// Superstep ss of a row: blocks 16 ss + 4 g .. + 3, those past the row's end zero.
+__device__ __forceinline__ void load_piece(Piece& p, const uint8_t* codes, const uint8_t* scales, int nblk, int ss,
+                                           int g) {
+  const int b0 = 16 * ss + 4 * g;
+  if (b0 + 4 <= nblk) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p.c[j] = *(const i32x4v*)(codes + (int64_t)(b0 + j) * 16);
+    __builtin_memcpy(&p.s, scales + b0, 4);
+  } else {
+    p.s = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      p.c[j] = i32x4v{0, 0, 0, 0};
+      if (b0 + j < nblk) {
+        p.c[j] = *(const i32x4v*)(codes + (int64_t)(b0 + j) * 16);
+        p.s |= (uint32_t)scales[b0 + j] << (8 * j);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ i32x8 wide(i32x4v v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+
+__device__ __forceinline__ f32x4 mfma4(const Piece& a, const Piece& b, f32x4 acc) {
+  acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(a.c[0]), wide(b.c[0]), acc, 4, 4, 0, a.s, 0, b.s);
+  acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(a.c[1]), wide(b.c[1]), acc, 4, 4, 1, a.s, 1, b.s);
+  acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(a.c[2]), wide(b.c[2]), acc, 4, 4, 2, a.s, 2, b.s);
+  acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(a.c[3]), wide(b.c[3]), acc, 4, 4, 3, a.s, 3, b.s);
+  return acc;
+}
+
+// Four consecutive outputs n .. n + 3 of one token.
+template <int DT>
+__device__ __forceinline__ void store_out(void* Y, int64_t ldy, int m, int n, int N, f32x4 v) {
+  uint16_t* y = (uint16_t*)Y + (int64_t)m * ldy + n;
+  const uint32_t lo = pack2(v[0], v[1], DT), hi = pack2(v[2], v[3], DT);
+  if (n + 4 <= N && ((uintptr_t)y & 7) == 0) {
+    *(uint2*)y = make_uint2(lo, hi);
+  } else {
+    if (n < N) y[0] = (uint16_t)lo;
+    if (n + 1 < N) y[1] = (uint16_t)(lo >> 16);
+    if (n + 2 < N) y[2] = (uint16_t)hi;
+    if (n + 3 < N) y[3] = (uint16_t)(hi >> 16);
+  }
+}
+
+// Few tokens: a workgroup owns 16 weight rows and 16 tokens; its 8 waves split
+// the contraction by supersteps and meet in LDS.
+template <int DT>
+__global__ __launch_bounds__(512) void k_mx_skinny(const ProductArgs a) {
+  __shared__ f32x4 part[8][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r16 = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
+  const int nblk = a.K / 32, nss = (nblk + 15) / 16;
+  const int64_t wr = min(n0 + r16, a.N - 1), xr = min(m0 + r16, a.M - 1);
+  const uint8_t* wc = a.wc + wr * (a.K / 2);
+  const uint8_t* ws = a.ws + wr * nblk;
+  const uint8_t* xc = a.xc + xr * (a.K / 2);
+  const uint8_t* xs = a.xs + xr * nblk;
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+  for (int ss = wave; ss < nss; ss += 8) {
+    Piece w, x;
+    load_piece(w, wc, ws, nblk, ss, g);
+    load_piece(x, xc, xs, nblk, ss, g);
+    acc = mfma4(w, x, acc);
+  }
+  part[wave][lane] = acc;
+  __syncthreads();
+  if (threadIdx.x < 64) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) acc += part[w][lane];
+    if (m0 + r16 < a.M) store_out<DT>(a.Y, a.ldy, m0 + r16, n0 + 4 * g, a.N, acc);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Launchers
+// ---------------------------------------------------------------------------
+void launch_quant(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes, uint8_t* scales,
+                  void* x_hat, hipStream_t st) {
+  QuantArgs a;
+  a.X = X;
+  a.ldx = ldx;
+  a.chunks = (uint32_t)(rows * (cols / 8));
+  a.row_chunks = (uint32_t)(cols / 8);
+  a.div = FastDiv::make(a.row_chunks);
+  a.codes = codes;
+  a.scales = scales;
+  a.x_hat = x_hat;
+  LaunchTimer t("mx_quant", st);
+  const dim3 grid((a.chunks + 255) / 256);
+  if (dtype == QAT_F32) QAT_LAUNCH(k_mx_quant<QAT_F32>, grid, dim3(256), 0, st, a);
+  else if (dtype == QAT_BF16) QAT_LAUNCH(k_mx_quant<QAT_BF16>, grid, dim3(256), 0, st, a);
+  else QAT_LAUNCH(k_mx_quant<QAT_F16>, grid, dim3(256), 0, st, a);
+}
+
+void launch_product(const ProductArgs& a, int dtype, hipStream_t st) {
+  LaunchTimer t("mx_gemm", st);
+  const dim3 grid((a.N + 15) / 16, (a.M + 15) / 16);
+  if (dtype == QAT_BF16) QAT_LAUNCH(k_mx_skinny<QAT_BF16>, grid, dim3(512), 0, st, a);
+  else QAT_LAUNCH(k_mx_skinny<QAT_F16>, grid, dim3(512), 0, st, a);
+}
+
+// The workspace of qat_mx_linear: X's codes, then its scales.
+struct MxWs {
+  size_t scales, bytes;
+  static MxWs of(int64_t M, int64_t in) {
+    MxWs w;
+    w.scales = (size_t)((M * in / 2 + 255) / 256 * 256);
+    w.bytes = w.scales + (size_t)((M * in / 32 + 255) / 256 * 256);
+    return w;
+  }
+};
+
+int32_t check_product(int64_t M, int64_t out, int64_t in, int32_t dtype, int64_t ldy) {
+  if (dtype != QAT_BF16 && dtype != QAT_F16) return QAT_ERR_TYPE;
+  if (M < 0 || out <= 0 || in <= 0 || in % 32 != 0) return QAT_ERR_SHAPE;
+  if (M > kMaxCount || out > kMaxCount || in > kMaxCount || ldy < out || ldy > kMaxCount) return QAT_ERR_SHAPE;
+  if (M * in * 2 > kMaxOperandBytes || out * in / 2 > kMaxOperandBytes || M * ldy * 2 > kMaxOperandBytes)
+    return QAT_ERR_SHAPE;
+  return QAT_OK;
+}
+
+}  // namespace
+}  // namespace qat
+
+QAT_API int32_t qat_mx_quant(const void* X, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes,
+                             uint8_t* scales, void* X_hat, hipStream_t stream) {
+  using namespace qat;
+  if (dtype < QAT_F32 || dtype > QAT_F16) return QAT_ERR_TYPE;
+  const int64_t e = dtype == QAT_F32 ? 4 : 2;
+  if (rows < 0 || cols <= 0 || cols % 32 != 0 || rows > kMaxCount || cols > kMaxCount || ldx < cols ||
+      ldx > kMaxCount || rows * (cols / 8) >= (int64_t(1) << 31))
+    return QAT_ERR_SHAPE;
+  if (rows == 0) return QAT_OK;
+  if (!X || (!codes && !X_hat) || !codes != !scales) return QAT_ERR_NULL;
+  if ((ldx * e) % 16 != 0) return QAT_ERR_ALIGN;
+  QAT_CHECK(check_aligned({X, codes, scales, X_hat}));
+  QAT_CHECK(check_spans({{codes, (size_t)(rows * cols / 2)}, {scales, (size_t)(rows * cols / 32)},
+                         {X_hat, (size_t)(rows * cols * e)}},
+                        {{X, strided_bytes(rows, ldx, cols, e)}}));
+  launch_quant(X, dtype, rows, cols, ldx, codes, scales, X_hat, stream);
+  return finish_call();
+}
+
+QAT_API size_t qat_mx_ws_bytes(int64_t M, int64_t out, int64_t in) {
+  using namespace qat;
+  if (check_product(M, out, in, QAT_BF16, out) != QAT_OK) return 0;
+  return MxWs::of(M, in).bytes;
+}
+
+QAT_API int32_t qat_mx_gemm(const uint8_t* X_codes, const uint8_t* X_scales, const uint8_t* W_codes,
+                            const uint8_t* W_scales, int64_t M, int64_t out, int64_t in, int32_t dtype, void* Y,
+                            int64_t ldy, void* ws, size_t ws_bytes, hipStream_t stream) {
+  using namespace qat;
+  (void)ws;
+  (void)ws_bytes;
+  QAT_CHECK(check_product(M, out, in, dtype, ldy));
+  if (M == 0) return QAT_OK;
+  QAT_CHECK(check_required({X_codes, X_scales, W_codes, W_scales, Y}));
+  QAT_CHECK(check_aligned({X_codes, X_scales, W_codes, W_scales, Y}));
+  QAT_CHECK(check_spans({{Y, strided_bytes(M, ldy, out, 2)}},
+                        {{X_codes, (size_t)(M * in / 2)}, {X_scales, (size_t)(M * in / 32)},
+                         {W_codes, (size_t)(out * in / 2)}, {W_scales, (size_t)(out * in / 32)}}));
+  ProductArgs a{X_codes, X_scales, W_codes, W_scales, (int)M, (int)out, (int)in, Y, ldy};
+  launch_product(a, dtype, stream);
+  return finish_call();
+}
+
+QAT_API int32_t qat_mx_linear(const void* X, int64_t ldx, const uint8_t* W_codes, const uint8_t* W_scales, int64_t M,
+                              int64_t out, int64_t in, int32_t dtype, void* Y, int64_t ldy, void* ws,
+                              size_t ws_bytes, hipStream_t stream) {
+  using namespace qat;
+  QAT_CHECK(check_product(M, out, in, dtype, ldy));
+  if (ldx < in || ldx > kMaxCount || M * ldx * 2 > kMaxOperandBytes) return QAT_ERR_SHAPE;
+  if (M == 0) return QAT_OK;
+  QAT_CHECK(check_required({X, W_codes, W_scales, Y}));
+  if (ldx % 8 != 0) return QAT_ERR_ALIGN;
+  QAT_CHECK(check_aligned({X, W_codes, W_scales, Y, ws}));
+  const MxWs w = MxWs::of(M, in);
+  if (!ws || ws_bytes < w.bytes) return QAT_ERR_WORKSPACE;
+  QAT_CHECK(check_spans({{Y, strided_bytes(M, ldy, out, 2)}, {ws, w.bytes}},
+                        {{X, strided_bytes(M, ldx, in, 2)}, {W_codes, (size_t)(out * in / 2)},
+                         {W_scales, (size_t)(out * in / 32)}}));
+  uint8_t* xc = (uint8_t*)ws;
+  uint8_t* xs = xc + w.scales;
+  launch_quant(X, dtype, M, in, ldx, xc, xs, nullptr, stream);
+  ProductArgs a{xc, xs, W_codes, W_scales, (int)M, (int)out, (int)in, Y, ldy};
+  launch_product(a, dtype, stream);
+  return finish_call();
+}
