@@ -20,7 +20,7 @@
  * - ldx, ldy: elements from one row to the next, at least the row's length;
  *   rows of X start 16-byte aligned (ldx * element size a multiple of 16);
  *   ldy is free;
- * - every operand of a product is smaller than 2 GiB.
+ * - a product's in is at most 2^20 and every operand smaller than 2 GiB.
  * Calls that share a workspace must not overlap in time.
  */
 #ifndef QAT_MX_H

@@ -450,18 +450,24 @@ I32 = (torch.int32,)
 
 
 class _RowArgs(_Args):
-    """_Args with row-strided activations and a launch on the tensors' device."""
+    """_Args with row-strided activations and a launch on the tensors' device.
+
+    A served token's calls take a few microseconds on the GPU, so the checks
+    ask each tensor for as little as they can and spell out an error only once
+    there is one.
+    """
+
+    def t(self, name: str, t, dtypes, shape=None, optional: bool = False, min_bytes: Optional[int] = None):
+        if isinstance(t, torch.Tensor) and (dtypes is None or t.dtype in dtypes) and min_bytes is None and (
+                shape is None or t.shape == shape) and t.is_contiguous():
+            self.seen.append((name, t))
+            return t.data_ptr()
+        return super().t(name, t, dtypes, shape, optional, min_bytes)
 
     def rows(self, name: str, t, dtypes, shape):
         """(pointer, elements between rows) of a tensor [rows, ...] whose trailing dimensions are contiguous."""
-        if t is None:
-            raise ValueError(f"{self.fn}: {name} is required")
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{self.fn}: {name} must be a torch.Tensor, got {type(t).__name__}")
-        if t.dtype not in dtypes:
-            raise TypeError(f"{self.fn}: {name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{self.fn}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape:
+            super().t(name, t, dtypes, shape)                # says what is wrong
         self.seen.append((name, t))
         row = math.prod(shape[1:])
         if t.is_contiguous():
@@ -477,13 +483,21 @@ class _RowArgs(_Args):
         return t.data_ptr(), ld
 
     def call(self, *args) -> None:
-        self.done()
-        dev = self.seen[0][1].device
-        if dev.index == torch.cuda.current_device():
-            _call(self.fn, *args, torch.cuda.current_stream(dev).cuda_stream)
+        dev = self.seen[0][1].get_device()
+        for _, t in self.seen:
+            if t.get_device() != dev or dev < 0:
+                self.done()                                  # says what is wrong
+        if dev == torch.cuda.current_device():
+            _call(self.fn, *args, _raw_stream(dev))
         else:
             with torch.cuda.device(dev):
-                _call(self.fn, *args, torch.cuda.current_stream(dev).cuda_stream)
+                _call(self.fn, *args, _raw_stream(dev))
+
+
+def _raw_stream(dev: int) -> int:
+    """The current stream's handle on a device, without a Stream object where torch offers that."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(dev) if get else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _dims(fn: str, name: str, t, n: int, what: str):

@@ -8,6 +8,7 @@
 #include "../../include/qat_mx.h"
 #include "qat_check.h"
 #include "qat_device.h"
+#include "qat_dma.h"
 #include "qat_internal.h"
 
 namespace qat {
@@ -15,7 +16,6 @@ namespace {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef int i32x4v __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // ---------------------------------------------------------------------------
@@ -145,7 +145,7 @@ __global__ __launch_bounds__(256) void k_mx_quant(const QuantArgs a) {
 // dword, whose byte j the instruction selects.
 // ---------------------------------------------------------------------------
 struct Piece {
-  i32x4v c[4];
+  i32x4 c[4];
   uint32_t s;
 };
 
@@ -165,22 +165,22 @@ __device__ __forceinline__ void load_piece(Piece& p, const uint8_t* codes, const
   const int b0 = 16 * ss + 4 * g;
   if (b0 + 4 <= nblk) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) p.c[j] = *(const i32x4v*)(codes + (int64_t)(b0 + j) * 16);
+    for (int j = 0; j < 4; ++j) p.c[j] = *(const i32x4*)(codes + (int64_t)(b0 + j) * 16);
     __builtin_memcpy(&p.s, scales + b0, 4);
   } else {
     p.s = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      p.c[j] = i32x4v{0, 0, 0, 0};
+      p.c[j] = i32x4{0, 0, 0, 0};
       if (b0 + j < nblk) {
-        p.c[j] = *(const i32x4v*)(codes + (int64_t)(b0 + j) * 16);
+        p.c[j] = *(const i32x4*)(codes + (int64_t)(b0 + j) * 16);
         p.s |= (uint32_t)scales[b0 + j] << (8 * j);
       }
     }
   }
 }
 
-__device__ __forceinline__ i32x8 wide(i32x4v v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+__device__ __forceinline__ i32x8 wide(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
 __device__ __forceinline__ f32x4 mfma4(const Piece& a, const Piece& b, f32x4 acc) {
   acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(a.c[0]), wide(b.c[0]), acc, 4, 4, 0, a.s, 0, b.s);
@@ -236,6 +236,154 @@ __global__ __launch_bounds__(512) void k_mx_skinny(const ProductArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// Many tokens: a workgroup of WM x WN waves owns TM tokens x TN weight rows and
+// walks the contraction in stages of 256 elements (128 bytes of codes and 8
+// scales a row) through LDS.
+//
+// Codes come by 16-byte DMA; chunk c (one block of 32) of row r sits at
+// c ^ (r & 7), so fragment reads use every bank equally. Scales come by 4-byte
+// DMA, three dwords a row from the aligned address at or before the row's 8
+// bytes (rows of in / 32 scales start at any byte); a lane reads its byte. A
+// row or a block past the end arrives as zero codes: rows by the buffer's
+// range, blocks by moving the lane out of it; their scales are set to zero on
+// reading, since what lies there may be 255.
+//
+// Two stages are resident. A stage has two steps of 128 elements; in the first
+// the second's fragments are read, in the second the next stage's first. In
+// between one barrier says that everyone has read all of this stage and that
+// the next has landed, and the loads of the stage after it go where this one
+// was: they have a whole stage to arrive.
+// ---------------------------------------------------------------------------
+template <int DT, int TM, int TN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_tile(const ProductArgs a) {
+  constexpr int NW = WM * WN, FM = TM / WM / 16, FN = TN / WN / 16;
+  constexpr int kCodes = (TM + TN) * 128, kStage = kCodes + (TM + TN) * 12;
+  constexpr int kDma = kCodes / 1024 / NW;                // 16-byte DMAs of a wave and stage
+  constexpr int kSDma = (TM + TN) * 3 / 64 / NW;          // 4-byte ones
+  static_assert(kDma * NW * 1024 == kCodes && kSDma * NW * 64 == (TM + TN) * 3, "whole instructions");
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int wm = wave / WN, wn = wave - wm * WN;
+  const int nblk = a.K / 32, S = (nblk + 7) / 8, ldk = a.K / 2;
+
+  // tile of this workgroup: consecutive tiles on one XCD, in bands of up to 4
+  // token tiles, so that the tiles an XCD works on together share both operands
+  const int tm = (a.M + TM - 1) / TM, tn = (a.N + TN - 1) / TN, T = tm * tn;
+  int id = blockIdx.x;
+  {
+    const int x = id & 7, q = T >> 3, r = T & 7;
+    id = x * q + min(x, r) + (id >> 3);
+  }
+  constexpr int kBand = 4;
+  const int band = id / (kBand * tn), in_band = id - band * kBand * tn;
+  const int h = min(kBand, tm - band * kBand);
+  const int m0 = (band * kBand + in_band % h) * TM, n0 = (in_band / h) * TN;
+
+  const i32x4 rx = buffer_rsrc(a.xc + (int64_t)m0 * ldk, (int64_t)min(TM, a.M - m0) * ldk);
+  const i32x4 rw = buffer_rsrc(a.wc + (int64_t)n0 * ldk, (int64_t)min(TN, a.N - n0) * ldk);
+  const i32x4 rxs = buffer_rsrc(a.xs, ((int64_t)a.M * nblk + 3) & ~3);
+  const i32x4 rws = buffer_rsrc(a.ws, ((int64_t)a.N * nblk + 3) & ~3);
+  const uint32_t lds0 = lds_addr_of(smem);
+  const int chunk = (lane & 7) ^ (lane >> 3);
+  const uint32_t vrow = (uint32_t)((lane >> 3) * ldk + chunk * 16);
+  uint32_t vs[kSDma];
+#pragma unroll
+  for (int i = 0; i < kSDma; ++i) {
+    const int q = (wave * kSDma + i) * 64 + lane, row = q / 3, part = q - 3 * row;
+    const bool is_x = row < TM;
+    vs[i] = (uint32_t)(((is_x ? m0 + row : n0 + row - TM) * nblk & ~3) + 4 * part);
+  }
+  auto issue = [&](int s) {
+    const uint32_t base = lds0 + (uint32_t)((s & 1) * kStage);
+    const uint32_t v0 = 8 * s + chunk < nblk ? vrow + (uint32_t)s * 128u : 0x7FFFFFF0u;
+#pragma unroll
+    for (int i = 0; i < kDma; ++i) {
+      const int k = wave * kDma + i;                      // 8 rows each: X's, then W's
+      const bool is_x = k < TM / 8;
+      dma16(is_x ? rx : rw, (uint32_t)__builtin_amdgcn_readfirstlane((int)(base + (uint32_t)k * 1024u)),
+            v0 + (uint32_t)((is_x ? k : k - TM / 8) * 8 * ldk));
+    }
+#pragma unroll
+    for (int i = 0; i < kSDma; ++i) {
+      const int k = wave * kSDma + i;                     // TM * 3 is a multiple of 64: one operand each
+      dma4(k < TM * 3 / 64 ? rxs : rws,
+           (uint32_t)__builtin_amdgcn_readfirstlane((int)(base + (uint32_t)(kCodes + k * 256))), vs[i] + (uint32_t)s * 8u);
+    }
+  };
+  static_assert(TM * 3 % 64 == 0, "one operand per scale DMA");
+
+  const int mis = r16 * nblk & 3;                         // of a row's scales behind the aligned address
+  const uint8_t* fx = smem + (wm * FM * 16 + r16) * 128;
+  const uint8_t* fw = smem + (TM + wn * FN * 16 + r16) * 128;
+  const uint8_t* sx = smem + kCodes + (wm * FM * 16 + r16) * 12 + mis + g;
+  const uint8_t* sw = smem + kCodes + (TM + wn * FN * 16 + r16) * 12 + mis + g;
+  const int cpos[2] = {(g ^ (r16 & 7)) << 4, ((4 + g) ^ (r16 & 7)) << 4};
+
+  struct Frags {
+    i32x4 x[FM], w[FN];
+    int xs[FM], ws[FN];
+  };
+  auto read = [&](Frags& f, int s, int j) {
+    const int off = (s & 1) * kStage;
+    const bool in = 8 * s + 4 * j + g < nblk;
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      f.w[i] = *(const i32x4*)(fw + off + i * 2048 + cpos[j]);
+      const int b = sw[off + i * 192 + 4 * j];
+      f.ws[i] = in ? b : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      f.x[i] = *(const i32x4*)(fx + off + i * 2048 + cpos[j]);
+      const int b = sx[off + i * 192 + 4 * j];
+      f.xs[i] = in ? b : 0;
+    }
+  };
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto product = [&](const Frags& f) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(f.w[j]), wide(f.x[i]), acc[i][j], 4, 4, 0,
+                                                                     f.ws[j], 0, f.xs[i]);
+  };
+
+  Frags p, q;
+  issue(0);
+  if (S > 1) {
+    issue(1);
+    wait_vmcnt<kDma + kSDma>();
+  } else {
+    wait_vmcnt<0>();
+  }
+  __syncthreads();
+  read(p, 0, 0);
+  for (int s = 0; s < S; ++s) {
+    read(q, s, 1);
+    product(p);
+    asm volatile("s_waitcnt lgkmcnt(0) vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (s + 2 < S) issue(s + 2);
+    read(p, s + 1, 0);
+    product(q);
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int m = m0 + (wm * FM + i) * 16 + r16;
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) store_out<DT>(a.Y, a.ldy, m, n0 + (wn * FN + j) * 16 + 4 * g, a.N, acc[i][j]);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
 void launch_quant(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes, uint8_t* scales,
@@ -256,8 +404,23 @@ void launch_quant(const void* X, int dtype, int64_t rows, int64_t cols, int64_t 
   else QAT_LAUNCH(k_mx_quant<QAT_F16>, grid, dim3(256), 0, st, a);
 }
 
+template <int DT, int TM, int TN, int WM, int WN>
+void launch_tile(const ProductArgs& a, hipStream_t st) {
+  constexpr int kLds = 2 * (TM + TN) * 140;
+  static const hipError_t raised = hipFuncSetAttribute((const void*)k_mx_tile<DT, TM, TN, WM, WN>,
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  (void)raised;                                           // a failure shows as the launch's error
+  const int64_t tiles = (int64_t)((a.M + TM - 1) / TM) * ((a.N + TN - 1) / TN);
+  QAT_LAUNCH((k_mx_tile<DT, TM, TN, WM, WN>), dim3((unsigned)tiles), dim3(64 * WM * WN), kLds, st, a);
+}
+
 void launch_product(const ProductArgs& a, int dtype, hipStream_t st) {
   LaunchTimer t("mx_gemm", st);
+  if (a.M > 128) {
+    if (dtype == QAT_BF16) launch_tile<QAT_BF16, 256, 256, 2, 2>(a, st);
+    else launch_tile<QAT_F16, 256, 256, 2, 2>(a, st);
+    return;
+  }
   const dim3 grid((a.N + 15) / 16, (a.M + 15) / 16);
   if (dtype == QAT_BF16) QAT_LAUNCH(k_mx_skinny<QAT_BF16>, grid, dim3(512), 0, st, a);
   else QAT_LAUNCH(k_mx_skinny<QAT_F16>, grid, dim3(512), 0, st, a);
@@ -277,7 +440,7 @@ struct MxWs {
 int32_t check_product(int64_t M, int64_t out, int64_t in, int32_t dtype, int64_t ldy) {
   if (dtype != QAT_BF16 && dtype != QAT_F16) return QAT_ERR_TYPE;
   if (M < 0 || out <= 0 || in <= 0 || in % 32 != 0) return QAT_ERR_SHAPE;
-  if (M > kMaxCount || out > kMaxCount || in > kMaxCount || ldy < out || ldy > kMaxCount) return QAT_ERR_SHAPE;
+  if (M > kMaxCount || out > kMaxCount || in > (1 << 20) || ldy < out || ldy > kMaxCount) return QAT_ERR_SHAPE;
   if (M * in * 2 > kMaxOperandBytes || out * in / 2 > kMaxOperandBytes || M * ldy * 2 > kMaxOperandBytes)
     return QAT_ERR_SHAPE;
   return QAT_OK;
