@@ -254,6 +254,23 @@ __global__ __launch_bounds__(512) void k_mx_skinny(const ProductArgs a) {
 // the next has landed, and the loads of the stage after it go where this one
 // was: they have a whole stage to arrive.
 // ---------------------------------------------------------------------------
+// One product step with its accumulator pinned to AGPRs (the compiler otherwise
+// moves accumulators between the two halves of the register file all the
+// time). The hazard recogniser does not look inside the asm: the sources are
+// LDS loads, which the compiler waits for, and scales selected at least two
+// products earlier; code that reads the accumulators first waits out the
+// instruction's latency (mfma_drain).
+__device__ __forceinline__ void mfma_acc(f32x4& c, const i32x4& w, const i32x4& x, int ws, int xs) {
+  asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+               : "+a"(c)
+               : "v"(w), "v"(x), "v"(ws), "v"(xs));
+}
+
+__device__ __forceinline__ void mfma_drain() {
+  asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 template <int DT, int TM, int TN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_tile(const ProductArgs a) {
   constexpr int NW = WM * WN, FM = TM / WM / 16, FN = TN / WN / 16;
@@ -294,21 +311,20 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_tile(const ProductArgs a
     const bool is_x = row < TM;
     vs[i] = (uint32_t)(((is_x ? m0 + row : n0 + row - TM) * nblk & ~3) + 4 * part);
   }
-  auto issue = [&](int s) {
+  // DMA number i of stage s: the 16-byte ones, then the scales'
+  auto issue = [&](int s, int i) {
     const uint32_t base = lds0 + (uint32_t)((s & 1) * kStage);
-    const uint32_t v0 = 8 * s + chunk < nblk ? vrow + (uint32_t)s * 128u : 0x7FFFFFF0u;
-#pragma unroll
-    for (int i = 0; i < kDma; ++i) {
+    if (i < kDma) {
+      const uint32_t v0 = 8 * s + chunk < nblk ? vrow + (uint32_t)s * 128u : 0x7FFFFFF0u;
       const int k = wave * kDma + i;                      // 8 rows each: X's, then W's
       const bool is_x = k < TM / 8;
       dma16(is_x ? rx : rw, (uint32_t)__builtin_amdgcn_readfirstlane((int)(base + (uint32_t)k * 1024u)),
             v0 + (uint32_t)((is_x ? k : k - TM / 8) * 8 * ldk));
-    }
-#pragma unroll
-    for (int i = 0; i < kSDma; ++i) {
-      const int k = wave * kSDma + i;                     // TM * 3 is a multiple of 64: one operand each
+    } else {
+      const int k = wave * kSDma + i - kDma;              // one operand each
       dma4(k < TM * 3 / 64 ? rxs : rws,
-           (uint32_t)__builtin_amdgcn_readfirstlane((int)(base + (uint32_t)(kCodes + k * 256))), vs[i] + (uint32_t)s * 8u);
+           (uint32_t)__builtin_amdgcn_readfirstlane((int)(base + (uint32_t)(kCodes + k * 256))),
+           vs[i - kDma] + (uint32_t)s * 8u);
     }
   };
   static_assert(TM * 3 % 64 == 0, "one operand per scale DMA");
@@ -324,62 +340,85 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_tile(const ProductArgs a
     i32x4 x[FM], w[FN];
     int xs[FM], ws[FN];
   };
-  auto read = [&](Frags& f, int s, int j) {
-    const int off = (s & 1) * kStage;
+  // read r of a step, in the order in which the products use them: w0, x0 .. x(FM-1), w1 ..
+  auto read = [&](Frags& f, int off, int j, int r) {
+    if (r == 0 || r > FM) {
+      const int i = r == 0 ? 0 : r - FM;
+      f.w[i] = *(const i32x4*)(fw + off + i * 2048 + cpos[j]);
+      f.ws[i] = sw[off + i * 192 + 4 * j];
+    } else {
+      f.x[r - 1] = *(const i32x4*)(fx + off + (r - 1) * 2048 + cpos[j]);
+      f.xs[r - 1] = sx[off + (r - 1) * 192 + 4 * j];
+    }
+  };
+  // scales of blocks past the end of the row
+  auto clear = [&](Frags& f, int s, int j) {
     const bool in = 8 * s + 4 * j + g < nblk;
 #pragma unroll
-    for (int i = 0; i < FN; ++i) {
-      f.w[i] = *(const i32x4*)(fw + off + i * 2048 + cpos[j]);
-      const int b = sw[off + i * 192 + 4 * j];
-      f.ws[i] = in ? b : 0;
-    }
+    for (int i = 0; i < FN; ++i) f.ws[i] = in ? f.ws[i] : 0;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      f.x[i] = *(const i32x4*)(fx + off + i * 2048 + cpos[j]);
-      const int b = sx[off + i * 192 + 4 * j];
-      f.xs[i] = in ? b : 0;
-    }
+    for (int i = 0; i < FM; ++i) f.xs[i] = in ? f.xs[i] : 0;
   };
-  f32x4 acc[FM][FN];
+  f32x4 acc[FN][FM];
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+  for (int j = 0; j < FN; ++j)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto product = [&](const Frags& f) {
+    for (int i = 0; i < FM; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  constexpr int NM = FM * FN, NR = FM + FN, ND = kDma + kSDma, kPer = (ND + NM - 1) / NM;
+  static_assert(NR <= NM - 2, "the next step's reads are issued before its scales are cleared");
+  // One step: product t, then read t of the next step (stage ns, half nj) and,
+  // with `dma`, a share of stage ns + 1's DMAs. The scales of the next step are
+  // cleared two products before the end, well after their reads and before
+  // their use. The fences keep this order: without them the compiler puts
+  // every read right before its use, and one wave a SIMD waits for it.
+  auto step = [&](const Frags& cur, Frags& nxt, int ns, int nj, bool dma) {
+    const int off = (ns & 1) * kStage;
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+    for (int t = 0; t < NM; ++t) {
+      const int j = t / FM, i = t % FM;
+      mfma_acc(acc[j][i], cur.w[j], cur.x[i], cur.ws[j], cur.xs[i]);
+      if (t < NR) read(nxt, off, nj, t);
+      if (dma) {
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(f.w[j]), wide(f.x[i]), acc[i][j], 4, 4, 0,
-                                                                     f.ws[j], 0, f.xs[i]);
+        for (int d = t * kPer; d < (t + 1) * kPer && d < ND; ++d) issue(ns + 1, d);
+      }
+      if (t == NM - 2) clear(nxt, ns, nj);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
 
+  // Stages past the last are loaded as zeros (their lanes are out of the row)
+  // and scales no one uses, so that every iteration is alike.
   Frags p, q;
-  issue(0);
-  if (S > 1) {
-    issue(1);
-    wait_vmcnt<kDma + kSDma>();
-  } else {
-    wait_vmcnt<0>();
-  }
+#pragma unroll
+  for (int i = 0; i < ND; ++i) issue(0, i);
+#pragma unroll
+  for (int i = 0; i < ND; ++i) issue(1, i);
+  wait_vmcnt<ND>();
   __syncthreads();
-  read(p, 0, 0);
+#pragma unroll
+  for (int r = 0; r < NR; ++r) read(p, 0, 0, r);
+  clear(p, 0, 0);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma clang loop unroll(disable)
   for (int s = 0; s < S; ++s) {
-    read(q, s, 1);
-    product(p);
-    asm volatile("s_waitcnt lgkmcnt(0) vmcnt(0)" ::: "memory");
+    step(p, q, s, 1, false);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // this wave has read all of stage s
+    wait_vmcnt<0>();                                      // its part of stage s + 1 has landed
     __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if (s + 2 < S) issue(s + 2);
-    read(p, s + 1, 0);
-    product(q);
+    __builtin_amdgcn_sched_barrier(0);
+    step(q, p, s + 1, 0, true);
+    // nothing behind the loop may read a result before it is written
+    if (s == S - 1) mfma_drain();
   }
+  wait_vmcnt<0>();                                        // the DMAs of stages past the last
+  mfma_drain();
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int m = m0 + (wm * FM + i) * 16 + r16;
     if (m >= a.M) continue;
 #pragma unroll
-    for (int j = 0; j < FN; ++j) store_out<DT>(a.Y, a.ldy, m, n0 + (wn * FN + j) * 16 + 4 * g, a.N, acc[i][j]);
+    for (int j = 0; j < FN; ++j) store_out<DT>(a.Y, a.ldy, m, n0 + (wn * FN + j) * 16 + 4 * g, a.N, acc[j][i]);
   }
 }
 
