@@ -3,7 +3,7 @@
 //
 // Format: 32 consecutive elements of a row share the scale 2^e (byte e + 127);
 // elements are E2M1 codes, two to a byte, the even element in the low half.
-#include <string.h>
+#include <type_traits>
 
 #include "../../include/qat_mx.h"
 #include "qat_check.h"
@@ -236,34 +236,86 @@ __global__ __launch_bounds__(512) void k_mx_skinny(const ProductArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: a workgroup of WM x WN waves owns TM tokens x TN weight rows and
-// walks the contraction in stages of 256 elements (128 bytes of codes and 8
-// scales a row) through LDS.
-//
-// Codes come by 16-byte DMA; chunk c (one block of 32) of row r sits at
-// c ^ (r & 7), so fragment reads use every bank equally. Scales come by 4-byte
-// DMA, three dwords a row from the aligned address at or before the row's 8
-// bytes (rows of in / 32 scales start at any byte); a lane reads its byte. A
-// row or a block past the end arrives as zero codes: rows by the buffer's
-// range, blocks by moving the lane out of it; their scales are set to zero on
-// reading, since what lies there may be 255.
-//
-// Two stages are resident. A stage has two steps of 128 elements; in the first
-// the second's fragments are read, in the second the next stage's first. In
-// between one barrier says that everyone has read all of this stage and that
-// the next has landed, and the loads of the stage after it go where this one
-// was: they have a whole stage to arrive.
+// Scales in the order of the tiled product: for each row and 512 elements (16
+// blocks, the last ones zero past the row's end) the bytes [g][j] of blocks
+// 4 j + g, so that lane group g has the scales of four steps in one dword.
+// What the zero scales (2^-127, of both operands) multiply is below 2^-245 and
+// vanishes, so codes past a row's end need no masking. One thread transposes
+// 16 bytes; a few microseconds beside the product, whose inner loop it frees of
+// byte reads, alignment and the ragged end.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ uint4 transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  // __builtin_amdgcn_perm(hi, lo, selector): bytes 0-3 of lo, 4-7 of hi
+  const uint32_t ab0 = __builtin_amdgcn_perm(b, a, 0x05010400u), ab1 = __builtin_amdgcn_perm(b, a, 0x07030602u);
+  const uint32_t cd0 = __builtin_amdgcn_perm(d, c, 0x05010400u), cd1 = __builtin_amdgcn_perm(d, c, 0x07030602u);
+  return make_uint4(__builtin_amdgcn_perm(cd0, ab0, 0x05040100u), __builtin_amdgcn_perm(cd0, ab0, 0x07060302u),
+                    __builtin_amdgcn_perm(cd1, ab1, 0x05040100u), __builtin_amdgcn_perm(cd1, ab1, 0x07060302u));
+}
+
+struct ReorderArgs {
+  const uint8_t* src[2];           // X's scales, W's
+  uint8_t* dst[2];
+  int64_t n0, n1;                  // 16-byte pieces of each
+  int nblk, nss;
+};
+
+__global__ __launch_bounds__(256) void k_mx_reorder(const ReorderArgs a) {
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int which = i >= a.n0;
+  if (which) i -= a.n0;
+  if (i >= (which ? a.n1 : a.n0)) return;
+  const int64_t row = i / a.nss;
+  const int b0 = (int)(i - row * a.nss) * 16, n = min(a.nblk - b0, 16);
+  const uint8_t* p = a.src[which] + row * a.nblk + b0;
+  uint32_t w[4] = {0, 0, 0, 0};
+  if (n == 16) {
+    __builtin_memcpy(w, p, 16);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (k < n) w[k >> 2] |= (uint32_t)p[k] << (8 * (k & 3));
+  }
+  *(uint4*)(a.dst[which] + i * 16) = transpose4(w[0], w[1], w[2], w[3]);
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens: a workgroup of WM x WN waves owns TM tokens x TN weight rows and
+// walks the contraction in stages of 256 elements (128 bytes of codes a row)
+// through LDS, NST stages resident; scales (reordered as above) come with
+// every second stage.
+//
+// Everything comes by 16-byte DMA. Chunk c (one block of 32) of row r sits at
+// c ^ (r & 7), so fragment reads use every bank equally. Rows past the end are
+// out of the buffer's range and arrive as zeros; from stage to stage only the
+// buffer's base and range move, not the lanes' offsets.
+//
+// A stage has two steps of 128 elements; in the first the second's fragments
+// are read, in the second the next stage's first. In between one barrier says
+// that everyone has read all of this stage and that the next has landed, and
+// the DMAs of the stage NST later go where this one was.
+//
+// With one wave a SIMD (256 x 256) a product takes 16 cycles of the matrix core
+// and 8 of the wave's issue, which leaves room for two other instructions: the
+// scales by dword, the DMAs' constant offsets and the scalar base are for that.
+// ---------------------------------------------------------------------------
+
 // One product step with its accumulator pinned to AGPRs (the compiler otherwise
 // moves accumulators between the two halves of the register file all the
-// time). The hazard recogniser does not look inside the asm: the sources are
-// LDS loads, which the compiler waits for, and scales selected at least two
-// products earlier; code that reads the accumulators first waits out the
-// instruction's latency (mfma_drain).
+// time); J selects the scales' byte. The hazard recogniser does not look
+// inside the asm: the sources are LDS loads, which the compiler waits for;
+// code that reads the accumulators first waits out the instruction's latency
+// (mfma_drain).
+template <int J>
 __device__ __forceinline__ void mfma_acc(f32x4& c, const i32x4& w, const i32x4& x, int ws, int xs) {
-  asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
-               : "+a"(c)
-               : "v"(w), "v"(x), "v"(ws), "v"(xs));
+#define QAT_MX_MFMA(SEL)                                                              \
+  asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " SEL " cbsz:4 blgp:4" \
+               : "+a"(c)                                                              \
+               : "v"(w), "v"(x), "v"(ws), "v"(xs))
+  if constexpr (J == 0) QAT_MX_MFMA("op_sel_hi:[0,0,0]");
+  else if constexpr (J == 1) QAT_MX_MFMA("op_sel:[1,1,0] op_sel_hi:[0,0,0]");
+  else if constexpr (J == 2) QAT_MX_MFMA("op_sel_hi:[1,1,0]");
+  else QAT_MX_MFMA("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
+#undef QAT_MX_MFMA
 }
 
 __device__ __forceinline__ void mfma_drain() {
@@ -271,18 +323,27 @@ __device__ __forceinline__ void mfma_drain() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int DT, int TM, int TN, int WM, int WN>
+template <int TM, int TN, int WM, int WN, int NST>
+struct TileShape {
+  static constexpr int kWaves = WM * WN, kRows = TM + TN;
+  static constexpr int kStage = kRows * 144;              // codes, then (even stages) scales
+  static constexpr int kLds = NST * kStage;
+  static constexpr int kDma = kRows / 8 / kWaves;         // 16-byte DMAs of a wave: a stage's codes
+  static constexpr int kSDma = kRows / 64 / kWaves;       // and a stage pair's scales
+  static_assert(kDma * kWaves * 8 == kRows && kSDma * kWaves * 64 == kRows, "whole instructions");
+  static_assert(TM % 64 == 0 && TN % 64 == 0 && NST % 2 == 0, "one operand for each DMA; stage pairs");
+  static_assert(kLds <= 160 * 1024, "LDS of a workgroup");
+};
+
+template <int DT, int TM, int TN, int WM, int WN, int NST>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_tile(const ProductArgs a) {
-  constexpr int NW = WM * WN, FM = TM / WM / 16, FN = TN / WN / 16;
-  constexpr int kCodes = (TM + TN) * 128, kStage = kCodes + (TM + TN) * 12;
-  constexpr int kDma = kCodes / 1024 / NW;                // 16-byte DMAs of a wave and stage
-  constexpr int kSDma = (TM + TN) * 3 / 64 / NW;          // 4-byte ones
-  static_assert(kDma * NW * 1024 == kCodes && kSDma * NW * 64 == (TM + TN) * 3, "whole instructions");
+  typedef TileShape<TM, TN, WM, WN, NST> TS;
+  constexpr int FM = TM / WM / 16, FN = TN / WN / 16;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   const int wm = wave / WN, wn = wave - wm * WN;
-  const int nblk = a.K / 32, S = (nblk + 7) / 8, ldk = a.K / 2;
+  const int ldk = a.K / 2, SS = (a.K + 511) / 512;        // stage pairs
 
   // tile of this workgroup: consecutive tiles on one XCD, in bands of up to 4
   // token tiles, so that the tiles an XCD works on together share both operands
@@ -296,120 +357,159 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_tile(const ProductArgs a
   const int band = id / (kBand * tn), in_band = id - band * kBand * tn;
   const int h = min(kBand, tm - band * kBand);
   const int m0 = (band * kBand + in_band % h) * TM, n0 = (in_band / h) * TN;
+  const int rows_x = min(TM, a.M - m0), rows_w = min(TN, a.N - n0);
 
-  const i32x4 rx = buffer_rsrc(a.xc + (int64_t)m0 * ldk, (int64_t)min(TM, a.M - m0) * ldk);
-  const i32x4 rw = buffer_rsrc(a.wc + (int64_t)n0 * ldk, (int64_t)min(TN, a.N - n0) * ldk);
-  const i32x4 rxs = buffer_rsrc(a.xs, ((int64_t)a.M * nblk + 3) & ~3);
-  const i32x4 rws = buffer_rsrc(a.ws, ((int64_t)a.N * nblk + 3) & ~3);
+  i32x4 rx = buffer_rsrc(a.xc + (int64_t)m0 * ldk, (int64_t)rows_x * ldk);
+  i32x4 rw = buffer_rsrc(a.wc + (int64_t)n0 * ldk, (int64_t)rows_w * ldk);
+  i32x4 rxs = buffer_rsrc(a.xs + (int64_t)m0 * SS * 16, (int64_t)rows_x * SS * 16);
+  i32x4 rws = buffer_rsrc(a.ws + (int64_t)n0 * SS * 16, (int64_t)rows_w * SS * 16);
+  // the next bytes of a buffer; empty once its end is passed
+  auto advance = [](i32x4& r, uint32_t by) {
+    const uint64_t b = ((uint64_t)(uint32_t)r[1] << 32 | (uint32_t)r[0]) + by;
+    r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)b);
+    r[1] = __builtin_amdgcn_readfirstlane((int)(b >> 32));
+    r[2] = __builtin_amdgcn_readfirstlane(max(r[2] - (int)by, 0));
+  };
   const uint32_t lds0 = lds_addr_of(smem);
-  const int chunk = (lane & 7) ^ (lane >> 3);
-  const uint32_t vrow = (uint32_t)((lane >> 3) * ldk + chunk * 16);
-  uint32_t vs[kSDma];
+  uint32_t vc[TS::kDma], vs[TS::kSDma];
 #pragma unroll
-  for (int i = 0; i < kSDma; ++i) {
-    const int q = (wave * kSDma + i) * 64 + lane, row = q / 3, part = q - 3 * row;
-    const bool is_x = row < TM;
-    vs[i] = (uint32_t)(((is_x ? m0 + row : n0 + row - TM) * nblk & ~3) + 4 * part);
+  for (int i = 0; i < TS::kDma; ++i) {
+    const int k = wave * TS::kDma + i, row = (k < TM / 8 ? k : k - TM / 8) * 8 + (lane >> 3);
+    vc[i] = (uint32_t)(row * ldk + (((lane & 7) ^ (lane >> 3)) << 4));
   }
-  // DMA number i of stage s: the 16-byte ones, then the scales'
-  auto issue = [&](int s, int i) {
-    const uint32_t base = lds0 + (uint32_t)((s & 1) * kStage);
-    if (i < kDma) {
-      const uint32_t v0 = 8 * s + chunk < nblk ? vrow + (uint32_t)s * 128u : 0x7FFFFFF0u;
-      const int k = wave * kDma + i;                      // 8 rows each: X's, then W's
-      const bool is_x = k < TM / 8;
-      dma16(is_x ? rx : rw, (uint32_t)__builtin_amdgcn_readfirstlane((int)(base + (uint32_t)k * 1024u)),
-            v0 + (uint32_t)((is_x ? k : k - TM / 8) * 8 * ldk));
+#pragma unroll
+  for (int i = 0; i < TS::kSDma; ++i) {
+    const int k = wave * TS::kSDma + i;
+    vs[i] = (uint32_t)(((k < TM / 64 ? k : k - TM / 64) * 64 + lane) * SS * 16);
+  }
+  // DMA i of the stage whose buffers rx .. rws stand at, into LDS stage `st`;
+  // from kDma on the stage pair's scales
+  auto issue = [&](uint32_t st, int i) {
+    if (i < TS::kDma) {
+      const int k = wave * TS::kDma + i;
+      dma16(k < TM / 8 ? rx : rw, (uint32_t)__builtin_amdgcn_readfirstlane((int)(st + (uint32_t)k * 1024u)), vc[i]);
     } else {
-      const int k = wave * kSDma + i - kDma;              // one operand each
-      dma4(k < TM * 3 / 64 ? rxs : rws,
-           (uint32_t)__builtin_amdgcn_readfirstlane((int)(base + (uint32_t)(kCodes + k * 256))),
-           vs[i - kDma] + (uint32_t)s * 8u);
+      const int k = wave * TS::kSDma + i - TS::kDma;
+      dma16(k < TM / 64 ? rxs : rws,
+            (uint32_t)__builtin_amdgcn_readfirstlane((int)(st + (uint32_t)(TS::kRows * 128 + k * 1024))),
+            vs[i - TS::kDma]);
     }
   };
-  static_assert(TM * 3 % 64 == 0, "one operand per scale DMA");
+  auto next_stage = [&](bool pair) {
+    advance(rx, 128);
+    advance(rw, 128);
+    if (pair) {
+      advance(rxs, 16);
+      advance(rws, 16);
+    }
+  };
 
-  const int mis = r16 * nblk & 3;                         // of a row's scales behind the aligned address
   const uint8_t* fx = smem + (wm * FM * 16 + r16) * 128;
   const uint8_t* fw = smem + (TM + wn * FN * 16 + r16) * 128;
-  const uint8_t* sx = smem + kCodes + (wm * FM * 16 + r16) * 12 + mis + g;
-  const uint8_t* sw = smem + kCodes + (TM + wn * FN * 16 + r16) * 12 + mis + g;
+  const uint8_t* sx = smem + TS::kRows * 128 + (wm * FM * 16 + r16) * 16 + 4 * g;
+  const uint8_t* sw = smem + TS::kRows * 128 + (TM + wn * FN * 16 + r16) * 16 + 4 * g;
   const int cpos[2] = {(g ^ (r16 & 7)) << 4, ((4 + g) ^ (r16 & 7)) << 4};
 
   struct Frags {
     i32x4 x[FM], w[FN];
-    int xs[FM], ws[FN];
+  };
+  struct Scales {
+    int x[FM], w[FN];
   };
   // read r of a step, in the order in which the products use them: w0, x0 .. x(FM-1), w1 ..
   auto read = [&](Frags& f, int off, int j, int r) {
-    if (r == 0 || r > FM) {
-      const int i = r == 0 ? 0 : r - FM;
-      f.w[i] = *(const i32x4*)(fw + off + i * 2048 + cpos[j]);
-      f.ws[i] = sw[off + i * 192 + 4 * j];
-    } else {
-      f.x[r - 1] = *(const i32x4*)(fx + off + (r - 1) * 2048 + cpos[j]);
-      f.xs[r - 1] = sx[off + (r - 1) * 192 + 4 * j];
-    }
+    if (r == 0) f.w[0] = *(const i32x4*)(fw + off + cpos[j]);
+    else if (r <= FM) f.x[r - 1] = *(const i32x4*)(fx + off + (r - 1) * 2048 + cpos[j]);
+    else f.w[r - FM] = *(const i32x4*)(fw + off + (r - FM) * 2048 + cpos[j]);
   };
-  // scales of blocks past the end of the row
-  auto clear = [&](Frags& f, int s, int j) {
-    const bool in = 8 * s + 4 * j + g < nblk;
-#pragma unroll
-    for (int i = 0; i < FN; ++i) f.ws[i] = in ? f.ws[i] : 0;
-#pragma unroll
-    for (int i = 0; i < FM; ++i) f.xs[i] = in ? f.xs[i] : 0;
+  auto read_scale = [&](Scales& f, int off, int r) {
+    if (r == 0) f.w[0] = *(const int*)(sw + off);
+    else if (r <= FM) f.x[r - 1] = *(const int*)(sx + off + (r - 1) * 256);
+    else f.w[r - FM] = *(const int*)(sw + off + (r - FM) * 256);
   };
   f32x4 acc[FN][FM];
 #pragma unroll
   for (int j = 0; j < FN; ++j)
 #pragma unroll
     for (int i = 0; i < FM; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  constexpr int NM = FM * FN, NR = FM + FN, ND = kDma + kSDma, kPer = (ND + NM - 1) / NM;
-  static_assert(NR <= NM - 2, "the next step's reads are issued before its scales are cleared");
-  // One step: product t, then read t of the next step (stage ns, half nj) and,
-  // with `dma`, a share of stage ns + 1's DMAs. The scales of the next step are
-  // cleared two products before the end, well after their reads and before
-  // their use. The fences keep this order: without them the compiler puts
-  // every read right before its use, and one wave a SIMD waits for it.
-  auto step = [&](const Frags& cur, Frags& nxt, int ns, int nj, bool dma) {
-    const int off = (ns & 1) * kStage;
+  constexpr int NM = FM * FN, NR = FM + FN;
+  static_assert(NR <= NM, "a step's reads fit its products");
+  // One step: product t with scale byte J, then read t of the next step (LDS
+  // stage at `off`, half nj; its scales too where a pair begins) and a share of
+  // the ND DMAs into LDS stage `st`. The fences keep this order: without them
+  // the compiler puts every read right before its use.
+  auto step = [&](auto jc, const Frags& cur, const Scales& sc, Frags& nxt, int off, int nj, auto nscale, Scales& nsc,
+                  auto nd, uint32_t st) {
+    constexpr int J = decltype(jc)::value, ND = decltype(nd)::value, kPer = (ND + NM - 1) / NM;
 #pragma unroll
     for (int t = 0; t < NM; ++t) {
       const int j = t / FM, i = t % FM;
-      mfma_acc(acc[j][i], cur.w[j], cur.x[i], cur.ws[j], cur.xs[i]);
-      if (t < NR) read(nxt, off, nj, t);
-      if (dma) {
-#pragma unroll
-        for (int d = t * kPer; d < (t + 1) * kPer && d < ND; ++d) issue(ns + 1, d);
+      mfma_acc<J>(acc[j][i], cur.w[j], cur.x[i], sc.w[j], sc.x[i]);
+      if (t < NR) {
+        read(nxt, off, nj, t);
+        if constexpr (decltype(nscale)::value) read_scale(nsc, off, t);
       }
-      if (t == NM - 2) clear(nxt, ns, nj);
+      // DMAs behind the reads, evenly
+      constexpr int kFirst = ND + NR <= NM ? NR : 0, kGap = ND ? (NM - kFirst) / ND : 0;
+      if constexpr (kGap > 0) {
+        if (t >= kFirst && (t - kFirst) % kGap == 0 && (t - kFirst) / kGap < ND) issue(st, (t - kFirst) / kGap);
+      } else {
+#pragma unroll
+        for (int d = t * kPer; d < (t + 1) * kPer && d < ND; ++d) issue(st, d);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-
-  // Stages past the last are loaded as zeros (their lanes are out of the row)
-  // and scales no one uses, so that every iteration is alike.
-  Frags p, q;
-#pragma unroll
-  for (int i = 0; i < ND; ++i) issue(0, i);
-#pragma unroll
-  for (int i = 0; i < ND; ++i) issue(1, i);
-  wait_vmcnt<ND>();
-  __syncthreads();
-#pragma unroll
-  for (int r = 0; r < NR; ++r) read(p, 0, 0, r);
-  clear(p, 0, 0);
-  __builtin_amdgcn_sched_barrier(0);
-#pragma clang loop unroll(disable)
-  for (int s = 0; s < S; ++s) {
-    step(p, q, s, 1, false);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // this wave has read all of stage s
-    wait_vmcnt<0>();                                      // its part of stage s + 1 has landed
+  constexpr std::integral_constant<int, 0> c0;
+  constexpr std::integral_constant<int, 1> c1;
+  constexpr std::integral_constant<int, 2> c2;
+  constexpr std::integral_constant<int, 3> c3;
+  constexpr std::integral_constant<int, TS::kDma> codes;
+  constexpr std::integral_constant<int, TS::kDma + TS::kSDma> codes_and_scales;
+  // DMAs in flight of stages behind the next one, at an even and an odd stage's barrier
+  constexpr int kFlight = (NST / 2 - 1) * (2 * TS::kDma + TS::kSDma);
+  auto landed = [&]() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // this wave has read all of the stage
+    wait_vmcnt<kFlight>();                                // its part of the next one has landed
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    step(q, p, s + 1, 0, true);
+  };
+
+  // Stages past the last are loaded as zeros (the buffers are empty) and
+  // multiply to nothing, so that every iteration is alike.
+#pragma unroll
+  for (int i = 0; i < NST; ++i) {
+    const uint32_t st = lds0 + (uint32_t)(i * TS::kStage);
+#pragma unroll
+    for (int d = 0; d < TS::kDma + (i % 2 ? 0 : TS::kSDma); ++d) issue(st, d);
+    next_stage(i % 2 == 0);
+  }
+  wait_vmcnt<(NST - 1) * TS::kDma + (NST / 2 - 1) * TS::kSDma>();
+  __syncthreads();
+  Frags p, q;
+  Scales sc, nsc;
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    read(p, 0, 0, r);
+    read_scale(sc, 0, r);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  int off = 0;                                            // LDS offset of the pair's even stage
+#pragma clang loop unroll(disable)
+  for (int ss = 0; ss < SS; ++ss) {
+    const int odd = off + TS::kStage, nxt = off + 2 * TS::kStage == TS::kLds ? 0 : off + 2 * TS::kStage;
+    step(c0, p, sc, q, off, 1, std::false_type{}, nsc, c0, 0u);
+    landed();
+    step(c1, q, sc, p, odd, 0, std::false_type{}, nsc, codes_and_scales, lds0 + (uint32_t)off);
+    next_stage(true);
+    step(c2, p, sc, q, odd, 1, std::false_type{}, nsc, c0, 0u);
+    landed();
+    step(c3, q, sc, p, nxt, 0, std::true_type{}, nsc, codes, lds0 + (uint32_t)odd);
+    next_stage(false);
+    sc = nsc;
+    off = nxt;
     // nothing behind the loop may read a result before it is written
-    if (s == S - 1) mfma_drain();
+    if (ss == SS - 1) mfma_drain();
   }
   wait_vmcnt<0>();                                        // the DMAs of stages past the last
   mfma_drain();
@@ -443,38 +543,62 @@ void launch_quant(const void* X, int dtype, int64_t rows, int64_t cols, int64_t 
   else QAT_LAUNCH(k_mx_quant<QAT_F16>, grid, dim3(256), 0, st, a);
 }
 
-template <int DT, int TM, int TN, int WM, int WN>
+// The product takes the tiled kernel from this many tokens on.
+constexpr int64_t kTileTokens = 128;
+
+template <int DT, int TM, int TN, int WM, int WN, int NST>
 void launch_tile(const ProductArgs& a, hipStream_t st) {
-  constexpr int kLds = 2 * (TM + TN) * 140;
-  static const hipError_t raised = hipFuncSetAttribute((const void*)k_mx_tile<DT, TM, TN, WM, WN>,
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-  (void)raised;                                           // a failure shows as the launch's error
+  typedef TileShape<TM, TN, WM, WN, NST> TS;
+  (void)hipFuncSetAttribute((const void*)k_mx_tile<DT, TM, TN, WM, WN, NST>,
+                            hipFuncAttributeMaxDynamicSharedMemorySize, TS::kLds);
   const int64_t tiles = (int64_t)((a.M + TM - 1) / TM) * ((a.N + TN - 1) / TN);
-  QAT_LAUNCH((k_mx_tile<DT, TM, TN, WM, WN>), dim3((unsigned)tiles), dim3(64 * WM * WN), kLds, st, a);
+  QAT_LAUNCH((k_mx_tile<DT, TM, TN, WM, WN, NST>), dim3((unsigned)tiles), dim3(64 * TS::kWaves), TS::kLds, st, a);
 }
 
-void launch_product(const ProductArgs& a, int dtype, hipStream_t st) {
-  LaunchTimer t("mx_gemm", st);
-  if (a.M > 128) {
-    if (dtype == QAT_BF16) launch_tile<QAT_BF16, 256, 256, 2, 2>(a, st);
-    else launch_tile<QAT_F16, 256, 256, 2, 2>(a, st);
+// Workspace: X's codes and scales (qat_mx_linear), and both operands' scales in
+// the tiled kernel's order.
+struct MxWs {
+  size_t xs, xr, wr, bytes;
+  static MxWs of(int64_t M, int64_t out, int64_t in, bool linear) {
+    auto up = [](int64_t v) { return (size_t)((v + 255) / 256 * 256); };
+    const int64_t row = (in + 511) / 512 * 16;
+    const bool tile = M > kTileTokens;
+    MxWs w;
+    w.xs = linear ? up(M * in / 2) : 0;
+    w.xr = w.xs + (linear ? up(M * in / 32) : 0);
+    w.wr = w.xr + (tile ? up(M * row) : 0);
+    w.bytes = w.wr + (tile ? up(out * row) : 0);
+    return w;
+  }
+};
+
+void launch_product(ProductArgs a, int dtype, uint8_t* ws, const MxWs& w, hipStream_t st) {
+  if (a.M > kTileTokens) {
+    ReorderArgs r;
+    r.nblk = a.K / 32;
+    r.nss = (r.nblk + 15) / 16;
+    r.src[0] = a.xs;
+    r.src[1] = a.ws;
+    r.dst[0] = ws + w.xr;
+    r.dst[1] = ws + w.wr;
+    r.n0 = (int64_t)a.M * r.nss;
+    r.n1 = (int64_t)a.N * r.nss;
+    {
+      LaunchTimer t("mx_reorder", st);
+      QAT_LAUNCH(k_mx_reorder, dim3((unsigned)((r.n0 + r.n1 + 255) / 256)), dim3(256), 0, st, r);
+    }
+    a.xs = r.dst[0];
+    a.ws = r.dst[1];
+    LaunchTimer t("mx_gemm", st);
+    if (dtype == QAT_BF16) launch_tile<QAT_BF16, 256, 256, 2, 2, 2>(a, st);
+    else launch_tile<QAT_F16, 256, 256, 2, 2, 2>(a, st);
     return;
   }
+  LaunchTimer t("mx_gemm", st);
   const dim3 grid((a.N + 15) / 16, (a.M + 15) / 16);
   if (dtype == QAT_BF16) QAT_LAUNCH(k_mx_skinny<QAT_BF16>, grid, dim3(512), 0, st, a);
   else QAT_LAUNCH(k_mx_skinny<QAT_F16>, grid, dim3(512), 0, st, a);
 }
-
-// The workspace of qat_mx_linear: X's codes, then its scales.
-struct MxWs {
-  size_t scales, bytes;
-  static MxWs of(int64_t M, int64_t in) {
-    MxWs w;
-    w.scales = (size_t)((M * in / 2 + 255) / 256 * 256);
-    w.bytes = w.scales + (size_t)((M * in / 32 + 255) / 256 * 256);
-    return w;
-  }
-};
 
 int32_t check_product(int64_t M, int64_t out, int64_t in, int32_t dtype, int64_t ldy) {
   if (dtype != QAT_BF16 && dtype != QAT_F16) return QAT_ERR_TYPE;
@@ -510,24 +634,24 @@ QAT_API int32_t qat_mx_quant(const void* X, int32_t dtype, int64_t rows, int64_t
 QAT_API size_t qat_mx_ws_bytes(int64_t M, int64_t out, int64_t in) {
   using namespace qat;
   if (check_product(M, out, in, QAT_BF16, out) != QAT_OK) return 0;
-  return MxWs::of(M, in).bytes;
+  return MxWs::of(M, out, in, true).bytes;
 }
 
 QAT_API int32_t qat_mx_gemm(const uint8_t* X_codes, const uint8_t* X_scales, const uint8_t* W_codes,
                             const uint8_t* W_scales, int64_t M, int64_t out, int64_t in, int32_t dtype, void* Y,
                             int64_t ldy, void* ws, size_t ws_bytes, hipStream_t stream) {
   using namespace qat;
-  (void)ws;
-  (void)ws_bytes;
   QAT_CHECK(check_product(M, out, in, dtype, ldy));
   if (M == 0) return QAT_OK;
+  const MxWs w = MxWs::of(M, out, in, false);
+  if (w.bytes && (!ws || ws_bytes < w.bytes)) return QAT_ERR_WORKSPACE;
   QAT_CHECK(check_required({X_codes, X_scales, W_codes, W_scales, Y}));
-  QAT_CHECK(check_aligned({X_codes, X_scales, W_codes, W_scales, Y}));
-  QAT_CHECK(check_spans({{Y, strided_bytes(M, ldy, out, 2)}},
+  QAT_CHECK(check_aligned({X_codes, X_scales, W_codes, W_scales, Y, ws}));
+  QAT_CHECK(check_spans({{Y, strided_bytes(M, ldy, out, 2)}, {ws, w.bytes}},
                         {{X_codes, (size_t)(M * in / 2)}, {X_scales, (size_t)(M * in / 32)},
                          {W_codes, (size_t)(out * in / 2)}, {W_scales, (size_t)(out * in / 32)}}));
   ProductArgs a{X_codes, X_scales, W_codes, W_scales, (int)M, (int)out, (int)in, Y, ldy};
-  launch_product(a, dtype, stream);
+  launch_product(a, dtype, (uint8_t*)ws, w, stream);
   return finish_call();
 }
 
@@ -541,15 +665,15 @@ QAT_API int32_t qat_mx_linear(const void* X, int64_t ldx, const uint8_t* W_codes
   QAT_CHECK(check_required({X, W_codes, W_scales, Y}));
   if (ldx % 8 != 0) return QAT_ERR_ALIGN;
   QAT_CHECK(check_aligned({X, W_codes, W_scales, Y, ws}));
-  const MxWs w = MxWs::of(M, in);
+  const MxWs w = MxWs::of(M, out, in, true);
   if (!ws || ws_bytes < w.bytes) return QAT_ERR_WORKSPACE;
   QAT_CHECK(check_spans({{Y, strided_bytes(M, ldy, out, 2)}, {ws, w.bytes}},
                         {{X, strided_bytes(M, ldx, in, 2)}, {W_codes, (size_t)(out * in / 2)},
                          {W_scales, (size_t)(out * in / 32)}}));
   uint8_t* xc = (uint8_t*)ws;
-  uint8_t* xs = xc + w.scales;
+  uint8_t* xs = xc + w.xs;
   launch_quant(X, dtype, M, in, ldx, xc, xs, nullptr, stream);
   ProductArgs a{xc, xs, W_codes, W_scales, (int)M, (int)out, (int)in, Y, ldy};
-  launch_product(a, dtype, stream);
+  launch_product(a, dtype, (uint8_t*)ws, w, stream);
   return finish_call();
 }
