@@ -205,6 +205,18 @@ __device__ __forceinline__ void store_out(void* Y, int64_t ldy, int m, int n, in
   }
 }
 
+// Eight of them.
+template <int DT>
+__device__ __forceinline__ void store_out8(void* Y, int64_t ldy, int m, int n, int N, f32x4 v, f32x4 w) {
+  uint16_t* y = (uint16_t*)Y + (int64_t)m * ldy + n;
+  if (n + 8 <= N && ((uintptr_t)y & 15) == 0) {
+    *(uint4*)y = make_uint4(pack2(v[0], v[1], DT), pack2(v[2], v[3], DT), pack2(w[0], w[1], DT), pack2(w[2], w[3], DT));
+  } else {
+    store_out<DT>(Y, ldy, m, n, N, v);
+    store_out<DT>(Y, ldy, m, n + 4, N, w);
+  }
+}
+
 // Few tokens: a workgroup owns 16 weight rows and 16 tokens; its 8 waves split
 // the contraction by supersteps and meet in LDS.
 template <int DT>
@@ -279,20 +291,27 @@ __global__ __launch_bounds__(256) void k_mx_reorder(const ReorderArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: a workgroup of WM x WN waves owns TM tokens x TN weight rows and
-// walks the contraction in stages of 256 elements (128 bytes of codes a row)
-// through LDS, NST stages resident; scales (reordered as above) come with
-// every second stage.
+// Many tokens: a workgroup of WM x WN waves owns tiles of TM tokens x TN weight
+// rows, one after the other, and walks the contraction through LDS in stages of
+// 256 elements (128 bytes of codes a row; with 64 bytes, half a line at a time,
+// the loads cost 12% of the whole) of two product steps. A group of two stages
+// shares the scales (reordered as above), which come with its first; NG groups
+// are resident.
 //
-// Everything comes by 16-byte DMA. Chunk c (one block of 32) of row r sits at
-// c ^ (r & 7), so fragment reads use every bank equally. Rows past the end are
-// out of the buffer's range and arrive as zeros; from stage to stage only the
-// buffer's base and range move, not the lanes' offsets.
+// Everything comes by 16-byte DMA. A lane's results are 8 consecutive outputs
+// of a token: row i = 4 a + b of weight fragments 2 j and 2 j + 1 is LDS row
+// 32 j + 8 a + b (+ 4), and chunk c (one block of 32) of an LDS row r sits at
+// c ^ (r & 3 | (r & 8) / 2), X's at c ^ (r & 7), so that fragment reads use
+// every bank equally. Rows past the end are out of the buffer's range and
+// arrive as zeros; from stage to stage only the buffer's base and range move,
+// not the lanes' offsets.
 //
-// A stage has two steps of 128 elements; in the first the second's fragments
-// are read, in the second the next stage's first. In between one barrier says
-// that everyone has read all of this stage and that the next has landed, and
-// the DMAs of the stage NST later go where this one was.
+// During a step the next step's fragments are read. The barrier in the middle
+// of a stage says that everyone has read all of it and that the next stage has
+// landed; the DMAs of the stage 2 NG later then go where this one was, early in
+// the step, and have most of two steps (of 1024 cycles at 256 x 256) to arrive.
+// Loads run on into the next tile, and a tile's stores are waited for with the
+// next tile's second stage.
 //
 // With one wave a SIMD (256 x 256) a product takes 16 cycles of the matrix core
 // and 8 of the wave's issue, which leaves room for two other instructions: the
@@ -323,46 +342,59 @@ __device__ __forceinline__ void mfma_drain() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int TM, int TN, int WM, int WN, int NST>
+template <int TM, int TN, int WM, int WN, int NG>
 struct TileShape {
   static constexpr int kWaves = WM * WN, kRows = TM + TN;
-  static constexpr int kStage = kRows * 144;              // codes, then (even stages) scales
-  static constexpr int kLds = NST * kStage;
-  static constexpr int kDma = kRows / 8 / kWaves;         // 16-byte DMAs of a wave: a stage's codes
-  static constexpr int kSDma = kRows / 64 / kWaves;       // and a stage pair's scales
-  static_assert(kDma * kWaves * 8 == kRows && kSDma * kWaves * 64 == kRows, "whole instructions");
-  static_assert(TM % 64 == 0 && TN % 64 == 0 && NST % 2 == 0, "one operand for each DMA; stage pairs");
+  static constexpr int kStage = kRows * 128;              // codes
+  static constexpr int kGroup = 2 * kStage + kRows * 16;  // two stages, then their scales
+  static constexpr int kLds = NG * kGroup;
+  static constexpr int kDma = kRows / 8 / kWaves;         // DMAs of a wave: a stage's codes
+  static constexpr int kSDma = (kRows / 64 + kWaves - 1) / kWaves;   // and a group's scales
+  static_assert(kDma * kWaves * 8 == kRows && TM % 64 == 0 && TN % 64 == 0, "whole DMAs, one operand each");
   static_assert(kLds <= 160 * 1024, "LDS of a workgroup");
+  static constexpr int kFlight = (NG - 1) * (2 * kDma + kSDma);      // DMAs behind the next stage at a barrier
+  static constexpr int kStores = TM * TN / 8 / 64 / kWaves;          // of a wave's results
 };
 
-template <int DT, int TM, int TN, int WM, int WN, int NST>
+template <int DT, int TM, int TN, int WM, int WN, int NG>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_tile(const ProductArgs a) {
-  typedef TileShape<TM, TN, WM, WN, NST> TS;
+  typedef TileShape<TM, TN, WM, WN, NG> TS;
   constexpr int FM = TM / WM / 16, FN = TN / WN / 16;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   const int wm = wave / WN, wn = wave - wm * WN;
-  const int ldk = a.K / 2, SS = (a.K + 511) / 512;        // stage pairs
+  const int ldk = a.K / 2, SS = (a.K + 511) / 512;        // groups
 
-  // tile of this workgroup: consecutive tiles on one XCD, in bands of up to 4
-  // token tiles, so that the tiles an XCD works on together share both operands
+  // Tiles of this workgroup: the grid has at most one workgroup for each CU and
+  // walks the tiles in rounds. Consecutive tiles are on one XCD, in bands of up
+  // to 4 token tiles, so that the tiles an XCD works on together share both
+  // operands; the last round is what is left.
   const int tm = (a.M + TM - 1) / TM, tn = (a.N + TN - 1) / TN, T = tm * tn;
-  int id = blockIdx.x;
-  {
-    const int x = id & 7, q = T >> 3, r = T & 7;
-    id = x * q + min(x, r) + (id >> 3);
-  }
-  constexpr int kBand = 4;
-  const int band = id / (kBand * tn), in_band = id - band * kBand * tn;
-  const int h = min(kBand, tm - band * kBand);
-  const int m0 = (band * kBand + in_band % h) * TM, n0 = (in_band / h) * TN;
-  const int rows_x = min(TM, a.M - m0), rows_w = min(TN, a.N - n0);
-
-  i32x4 rx = buffer_rsrc(a.xc + (int64_t)m0 * ldk, (int64_t)rows_x * ldk);
-  i32x4 rw = buffer_rsrc(a.wc + (int64_t)n0 * ldk, (int64_t)rows_w * ldk);
-  i32x4 rxs = buffer_rsrc(a.xs + (int64_t)m0 * SS * 16, (int64_t)rows_x * SS * 16);
-  i32x4 rws = buffer_rsrc(a.ws + (int64_t)n0 * SS * 16, (int64_t)rows_w * SS * 16);
+  const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+  const int xcd_tiles = (T >> 3) + (xcd < (T & 7) ? 1 : 0), xcd_first = xcd * (T >> 3) + min(xcd, T & 7);
+  const int xcd_slots = ((int)gridDim.x + 7 - xcd) >> 3;
+  auto tile_at = [&](int k, int& m0, int& n0) {           // tile k of this workgroup; false past its last
+    const int local = k * xcd_slots + slot;
+    if (local >= xcd_tiles) return false;
+    constexpr int kBand = 4;
+    const int id = xcd_first + local;
+    const int band = id / (kBand * tn), in_band = id - band * kBand * tn;
+    const int h = min(kBand, tm - band * kBand);
+    m0 = (band * kBand + in_band % h) * TM;
+    n0 = (in_band / h) * TN;
+    return true;
+  };
+  i32x4 rx, rw, rxs, rws;
+  auto open = [&](int k) {                                // the buffers at the start of tile k, or empty
+    int m = 0, n = 0;
+    const bool any = tile_at(k, m, n);
+    const int rows_x = any ? min(TM, a.M - m) : 0, rows_w = any ? min(TN, a.N - n) : 0;
+    rx = buffer_rsrc(a.xc + (int64_t)m * ldk, (int64_t)rows_x * ldk);
+    rw = buffer_rsrc(a.wc + (int64_t)n * ldk, (int64_t)rows_w * ldk);
+    rxs = buffer_rsrc(a.xs + (int64_t)m * SS * 16, (int64_t)rows_x * SS * 16);
+    rws = buffer_rsrc(a.ws + (int64_t)n * SS * 16, (int64_t)rows_w * SS * 16);
+  };
   // the next bytes of a buffer; empty once its end is passed
   auto advance = [](i32x4& r, uint32_t by) {
     const uint64_t b = ((uint64_t)(uint32_t)r[1] << 32 | (uint32_t)r[0]) + by;
@@ -371,44 +403,55 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_tile(const ProductArgs a
     r[2] = __builtin_amdgcn_readfirstlane(max(r[2] - (int)by, 0));
   };
   const uint32_t lds0 = lds_addr_of(smem);
+  // DMA k of a stage moves rows 8 k .. + 7 (X's, then W's); lane l lands at row
+  // l / 8, position l % 8, and fetches the chunk that this position holds
   uint32_t vc[TS::kDma], vs[TS::kSDma];
 #pragma unroll
   for (int i = 0; i < TS::kDma; ++i) {
-    const int k = wave * TS::kDma + i, row = (k < TM / 8 ? k : k - TM / 8) * 8 + (lane >> 3);
-    vc[i] = (uint32_t)(row * ldk + (((lane & 7) ^ (lane >> 3)) << 4));
+    const int k = wave * TS::kDma + i, r = lane >> 3;
+    const bool is_x = k < TM / 8;
+    const int row = (is_x ? k : k - TM / 8) * 8 + r, sw = is_x ? r : (r & 3) | (row & 8) >> 1;
+    vc[i] = (uint32_t)(row * ldk + (((lane & 7) ^ sw) << 4));
   }
 #pragma unroll
   for (int i = 0; i < TS::kSDma; ++i) {
     const int k = wave * TS::kSDma + i;
     vs[i] = (uint32_t)(((k < TM / 64 ? k : k - TM / 64) * 64 + lane) * SS * 16);
   }
-  // DMA i of the stage whose buffers rx .. rws stand at, into LDS stage `st`;
-  // from kDma on the stage pair's scales
-  auto issue = [&](uint32_t st, int i) {
+  // DMA i of the stage at which the buffers rx .. rws stand, into the LDS group
+  // at `grp` as its stage j; from kDma on the group's scales
+  auto issue = [&](uint32_t grp, int j, int i) {
     if (i < TS::kDma) {
       const int k = wave * TS::kDma + i;
-      dma16(k < TM / 8 ? rx : rw, (uint32_t)__builtin_amdgcn_readfirstlane((int)(st + (uint32_t)k * 1024u)), vc[i]);
+      dma16(k < TM / 8 ? rx : rw,
+            (uint32_t)__builtin_amdgcn_readfirstlane((int)(grp + (uint32_t)(j * TS::kStage + k * 1024))), vc[i]);
     } else {
-      const int k = wave * TS::kSDma + i - TS::kDma;
+      // a wave without a share repeats the last one, so that all waves count alike
+      const int k = min(wave * TS::kSDma + i - TS::kDma, TS::kRows / 64 - 1);
+      const uint32_t v = (TS::kRows / 64) % TS::kWaves == 0 ? vs[i - TS::kDma]
+                                                            : (uint32_t)(((k < TM / 64 ? k : k - TM / 64) * 64 + lane) * SS * 16);
       dma16(k < TM / 64 ? rxs : rws,
-            (uint32_t)__builtin_amdgcn_readfirstlane((int)(st + (uint32_t)(TS::kRows * 128 + k * 1024))),
-            vs[i - TS::kDma]);
+            (uint32_t)__builtin_amdgcn_readfirstlane((int)(grp + (uint32_t)(2 * TS::kStage + k * 1024))), v);
     }
   };
-  auto next_stage = [&](bool pair) {
+  auto next_stage = [&](bool group) {
     advance(rx, 128);
     advance(rw, 128);
-    if (pair) {
+    if (group) {
       advance(rxs, 16);
       advance(rws, 16);
     }
   };
 
+  // step parity h of a stage: lane group g has chunk 4 h + g; weight fragments
+  // 2 j + b are 32 j + 4 b rows in, with rows 8 (r16 / 4) + r16 % 4
+  const int wrow = 8 * (r16 >> 2) + (r16 & 3), wsw = (r16 & 3) | (r16 & 4);
+  const int xpos[2] = {(g ^ (r16 & 7)) << 4, ((4 + g) ^ (r16 & 7)) << 4};
+  const int wpos[2] = {(g ^ wsw) << 4, ((4 + g) ^ wsw) << 4};
   const uint8_t* fx = smem + (wm * FM * 16 + r16) * 128;
-  const uint8_t* fw = smem + (TM + wn * FN * 16 + r16) * 128;
-  const uint8_t* sx = smem + TS::kRows * 128 + (wm * FM * 16 + r16) * 16 + 4 * g;
-  const uint8_t* sw = smem + TS::kRows * 128 + (TM + wn * FN * 16 + r16) * 16 + 4 * g;
-  const int cpos[2] = {(g ^ (r16 & 7)) << 4, ((4 + g) ^ (r16 & 7)) << 4};
+  const uint8_t* fw = smem + (TM + wn * FN * 16 + wrow) * 128;
+  const uint8_t* sx = smem + 2 * TS::kStage + (wm * FM * 16 + r16) * 16 + 4 * g;
+  const uint8_t* sw = smem + 2 * TS::kStage + (TM + wn * FN * 16 + wrow) * 16 + 4 * g;
 
   struct Frags {
     i32x4 x[FM], w[FN];
@@ -417,74 +460,85 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_tile(const ProductArgs a
     int x[FM], w[FN];
   };
   // read r of a step, in the order in which the products use them: w0, x0 .. x(FM-1), w1 ..
-  auto read = [&](Frags& f, int off, int j, int r) {
-    if (r == 0) f.w[0] = *(const i32x4*)(fw + off + cpos[j]);
-    else if (r <= FM) f.x[r - 1] = *(const i32x4*)(fx + off + (r - 1) * 2048 + cpos[j]);
-    else f.w[r - FM] = *(const i32x4*)(fw + off + (r - FM) * 2048 + cpos[j]);
+  auto read = [&](Frags& f, int off, int h, int r) {
+    if (r >= 1 && r <= FM) {
+      f.x[r - 1] = *(const i32x4*)(fx + off + xpos[h] + (r - 1) * 2048);
+    } else {
+      const int i = r ? r - FM : 0;
+      f.w[i] = *(const i32x4*)(fw + off + wpos[h] + (32 * (i >> 1) + 4 * (i & 1)) * 128);
+    }
   };
   auto read_scale = [&](Scales& f, int off, int r) {
-    if (r == 0) f.w[0] = *(const int*)(sw + off);
-    else if (r <= FM) f.x[r - 1] = *(const int*)(sx + off + (r - 1) * 256);
-    else f.w[r - FM] = *(const int*)(sw + off + (r - FM) * 256);
+    if (r >= 1 && r <= FM) {
+      f.x[r - 1] = *(const int*)(sx + off + (r - 1) * 256);
+    } else {
+      const int i = r ? r - FM : 0;
+      f.w[i] = *(const int*)(sw + off + (32 * (i >> 1) + 4 * (i & 1)) * 16);
+    }
   };
   f32x4 acc[FN][FM];
-#pragma unroll
-  for (int j = 0; j < FN; ++j)
-#pragma unroll
-    for (int i = 0; i < FM; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   constexpr int NM = FM * FN, NR = FM + FN;
   static_assert(NR <= NM, "a step's reads fit its products");
-  // One step: product t with scale byte J, then read t of the next step (LDS
-  // stage at `off`, half nj; its scales too where a pair begins) and a share of
-  // the ND DMAs into LDS stage `st`. The fences keep this order: without them
-  // the compiler puts every read right before its use.
-  auto step = [&](auto jc, const Frags& cur, const Scales& sc, Frags& nxt, int off, int nj, auto nscale, Scales& nsc,
-                  auto nd, uint32_t st) {
-    constexpr int J = decltype(jc)::value, ND = decltype(nd)::value, kPer = (ND + NM - 1) / NM;
+  // Step J of a group (scale byte J): product t, then a share of the DMAs (odd
+  // steps, into stage J / 2 of the group at `grp`) and, behind them, the reads of
+  // the next step (from LDS offset `off`; its scales too where a group begins).
+  // The fences keep this order: without them the compiler puts every read right
+  // before its use.
+  auto step = [&](auto jc, const Frags& cur, const Scales& sc, Frags& nxt, int off, Scales& nsc, int soff,
+                  uint32_t grp) {
+    constexpr int J = decltype(jc)::value;
+    constexpr int ND = J % 2 == 0 ? 0 : TS::kDma + (J == 1 ? TS::kSDma : 0);
+    constexpr int kOps = ND + NR, kPer = (kOps + NM - 1) / NM;        // memory operations of a product
 #pragma unroll
     for (int t = 0; t < NM; ++t) {
       const int j = t / FM, i = t % FM;
       mfma_acc<J>(acc[j][i], cur.w[j], cur.x[i], sc.w[j], sc.x[i]);
-      if (t < NR) {
-        read(nxt, off, nj, t);
-        if constexpr (decltype(nscale)::value) read_scale(nsc, off, t);
-      }
-      // DMAs behind the reads, evenly
-      constexpr int kFirst = ND + NR <= NM ? NR : 0, kGap = ND ? (NM - kFirst) / ND : 0;
-      if constexpr (kGap > 0) {
-        if (t >= kFirst && (t - kFirst) % kGap == 0 && (t - kFirst) / kGap < ND) issue(st, (t - kFirst) / kGap);
-      } else {
 #pragma unroll
-        for (int d = t * kPer; d < (t + 1) * kPer && d < ND; ++d) issue(st, d);
+      for (int o = t * kPer; o < (t + 1) * kPer && o < kOps; ++o) {
+        if (o < ND) {
+          issue(grp, J / 2, o);
+        } else {
+          read(nxt, off, (J + 1) % 2, o - ND);
+          if constexpr (J == 3) read_scale(nsc, soff, o - ND);
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (J % 2) next_stage(J == 1);
+  };
+  // the barrier in a stage's middle; `stores`: a tile's stores are behind the next stage's DMAs
+  auto landed = [&](bool stores) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // this wave has read all of the stage
+    constexpr int kMost = TS::kFlight + TS::kStores < 63 ? TS::kFlight + TS::kStores : 63;
+    if (stores) wait_vmcnt<kMost>();
+    else wait_vmcnt<TS::kFlight>();                       // its part of the next one has landed
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
   };
   constexpr std::integral_constant<int, 0> c0;
   constexpr std::integral_constant<int, 1> c1;
   constexpr std::integral_constant<int, 2> c2;
   constexpr std::integral_constant<int, 3> c3;
-  constexpr std::integral_constant<int, TS::kDma> codes;
-  constexpr std::integral_constant<int, TS::kDma + TS::kSDma> codes_and_scales;
-  // DMAs in flight of stages behind the next one, at an even and an odd stage's barrier
-  constexpr int kFlight = (NST / 2 - 1) * (2 * TS::kDma + TS::kSDma);
-  auto landed = [&]() {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // this wave has read all of the stage
-    wait_vmcnt<kFlight>();                                // its part of the next one has landed
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-  };
 
-  // Stages past the last are loaded as zeros (the buffers are empty) and
-  // multiply to nothing, so that every iteration is alike.
+  // The loads run on from one tile into the next (and past the last tile from
+  // empty buffers, as zeros): the next tile's first groups arrive while this
+  // one's last are multiplied and its results are stored.
+  int ahead = 0, ahead_ss = 0;                            // tile and group at which the buffers stand
+  auto next_group = [&]() {
+    if (++ahead_ss == SS) {
+      ahead_ss = 0;
+      open(++ahead);
+    }
+  };
+  open(0);
 #pragma unroll
-  for (int i = 0; i < NST; ++i) {
-    const uint32_t st = lds0 + (uint32_t)(i * TS::kStage);
+  for (int i = 0; i < 2 * NG; ++i) {
 #pragma unroll
-    for (int d = 0; d < TS::kDma + (i % 2 ? 0 : TS::kSDma); ++d) issue(st, d);
+    for (int d = 0; d < TS::kDma + (i % 2 ? 0 : TS::kSDma); ++d) issue(lds0 + (uint32_t)(i / 2 * TS::kGroup), i % 2, d);
     next_stage(i % 2 == 0);
+    if (i % 2) next_group();
   }
-  wait_vmcnt<(NST - 1) * TS::kDma + (NST / 2 - 1) * TS::kSDma>();
+  wait_vmcnt<TS::kFlight + TS::kDma>();                   // stage 0
   __syncthreads();
   Frags p, q;
   Scales sc, nsc;
@@ -494,32 +548,45 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_tile(const ProductArgs a
     read_scale(sc, 0, r);
   }
   __builtin_amdgcn_sched_barrier(0);
-  int off = 0;                                            // LDS offset of the pair's even stage
+  int off = 0;                                            // LDS offset of the group
+  bool stores = false;                                    // the last tile's, all of kStores or more, may be on their way
+  int m0, n0;
+  for (int k = 0; tile_at(k, m0, n0); ++k) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int i = 0; i < FM; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    mfma_drain();                                         // written before the first product reads them
 #pragma clang loop unroll(disable)
-  for (int ss = 0; ss < SS; ++ss) {
-    const int odd = off + TS::kStage, nxt = off + 2 * TS::kStage == TS::kLds ? 0 : off + 2 * TS::kStage;
-    step(c0, p, sc, q, off, 1, std::false_type{}, nsc, c0, 0u);
-    landed();
-    step(c1, q, sc, p, odd, 0, std::false_type{}, nsc, codes_and_scales, lds0 + (uint32_t)off);
-    next_stage(true);
-    step(c2, p, sc, q, odd, 1, std::false_type{}, nsc, c0, 0u);
-    landed();
-    step(c3, q, sc, p, nxt, 0, std::true_type{}, nsc, codes, lds0 + (uint32_t)odd);
-    next_stage(false);
-    sc = nsc;
-    off = nxt;
-    // nothing behind the loop may read a result before it is written
-    if (ss == SS - 1) mfma_drain();
-  }
-  wait_vmcnt<0>();                                        // the DMAs of stages past the last
-  mfma_drain();
+    for (int ss = 0; ss < SS; ++ss) {
+      const int nxt = NG == 1 || off == (NG - 1) * TS::kGroup ? 0 : off + TS::kGroup;
+      const uint32_t grp = lds0 + (uint32_t)off;
+      step(c0, p, sc, q, off, nsc, 0, grp);
+      landed(stores && ss == 0);
+      step(c1, q, sc, p, off + TS::kStage, nsc, 0, grp);
+      step(c2, p, sc, q, off + TS::kStage, nsc, 0, grp);
+      landed(false);
+      step(c3, q, sc, p, nxt, nsc, nxt, grp);
+      next_group();
+      sc = nsc;
+      off = nxt;
+      // nothing behind the loop may read a result before it is written
+      if (ss == SS - 1) mfma_drain();
+    }
+    mfma_drain();
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int m = m0 + (wm * FM + i) * 16 + r16;
-    if (m >= a.M) continue;
+    for (int i = 0; i < FM; ++i) {
+      const int m = m0 + (wm * FM + i) * 16 + r16;
+      if (m < a.M) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j) store_out<DT>(a.Y, a.ldy, m, n0 + (wn * FN + j) * 16 + 4 * g, a.N, acc[j][i]);
+        for (int j = 0; j < FN; j += 2)
+          store_out8<DT>(a.Y, a.ldy, m, n0 + (wn * FN + j) * 16 + 8 * g, a.N, acc[j][i], acc[j + 1][i]);
+      }
+    }
+    // a tile over the edge may have stored less: then the count would not hold
+    stores = m0 + TM <= a.M && n0 + TN <= a.N;
   }
+  wait_vmcnt<0>();                                        // the DMAs past the last tile
 }
 
 // ---------------------------------------------------------------------------
@@ -543,16 +610,31 @@ void launch_quant(const void* X, int dtype, int64_t rows, int64_t cols, int64_t 
   else QAT_LAUNCH(k_mx_quant<QAT_F16>, grid, dim3(256), 0, st, a);
 }
 
+// Compute units of the current device.
+int num_cus() {
+  static int cached[64] = {0};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  if (!cached[dev]) {
+    int n = 0;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
+    cached[dev] = n;
+  }
+  return cached[dev];
+}
+
 // The product takes the tiled kernel from this many tokens on.
 constexpr int64_t kTileTokens = 128;
 
-template <int DT, int TM, int TN, int WM, int WN, int NST>
+template <int DT, int TM, int TN, int WM, int WN, int NG>
 void launch_tile(const ProductArgs& a, hipStream_t st) {
-  typedef TileShape<TM, TN, WM, WN, NST> TS;
-  (void)hipFuncSetAttribute((const void*)k_mx_tile<DT, TM, TN, WM, WN, NST>,
+  typedef TileShape<TM, TN, WM, WN, NG> TS;
+  (void)hipFuncSetAttribute((const void*)k_mx_tile<DT, TM, TN, WM, WN, NG>,
                             hipFuncAttributeMaxDynamicSharedMemorySize, TS::kLds);
   const int64_t tiles = (int64_t)((a.M + TM - 1) / TM) * ((a.N + TN - 1) / TN);
-  QAT_LAUNCH((k_mx_tile<DT, TM, TN, WM, WN, NST>), dim3((unsigned)tiles), dim3(64 * TS::kWaves), TS::kLds, st, a);
+  const int64_t slots = (int64_t)num_cus() * (160 * 1024 / TS::kLds);
+  QAT_LAUNCH((k_mx_tile<DT, TM, TN, WM, WN, NG>), dim3((unsigned)(tiles < slots ? tiles : slots)),
+             dim3(64 * TS::kWaves), TS::kLds, st, a);
 }
 
 // Workspace: X's codes and scales (qat_mx_linear), and both operands' scales in
@@ -590,8 +672,8 @@ void launch_product(ProductArgs a, int dtype, uint8_t* ws, const MxWs& w, hipStr
     a.xs = r.dst[0];
     a.ws = r.dst[1];
     LaunchTimer t("mx_gemm", st);
-    if (dtype == QAT_BF16) launch_tile<QAT_BF16, 256, 256, 2, 2, 2>(a, st);
-    else launch_tile<QAT_F16, 256, 256, 2, 2, 2>(a, st);
+    if (dtype == QAT_BF16) launch_tile<QAT_BF16, 256, 256, 2, 2, 1>(a, st);
+    else launch_tile<QAT_F16, 256, 256, 2, 2, 1>(a, st);
     return;
   }
   LaunchTimer t("mx_gemm", st);
