@@ -133,6 +133,10 @@ GEMM = [
     (17, 130, 1056), (31, 65, 2080), (33, 512, 128), (64, 300, 4096), (65, 257, 160), (77, 1024, 3584), (128, 128, 256),
     (129, 255, 288), (200, 511, 4128), (256, 256, 2048), (300, 770, 1568), (512, 1030, 1024), (1000, 129, 8192),
     (257, 4100, 480),
+    # the tiled kernels: 64 x 64, 128 x 128 with two groups and one, 256 x 256; ragged rows, columns and
+    # contractions, and several tiles for a workgroup
+    (33, 4100, 4640), (333, 1031, 4640), (1030, 2100, 1056), (1500, 1900, 2080), (2100, 3001, 544), (2300, 3008, 1536),
+    (4129, 4100, 288), (4096, 4864, 1056), (5000, 4099, 32),
 ]
 
 

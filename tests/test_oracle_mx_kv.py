@@ -7,6 +7,7 @@ import torch
 
 from oracle import kv_oracle as KV
 from oracle import mx_oracle as MX
+from tests.test_isa_hazard import _device_asm, _hipcc, accumulator_hazards
 from weight_quantization_aware_amd import _lib as Q
 
 FAKE = 1 << 20
@@ -219,3 +220,11 @@ def test_binding_refuses_wrong_tensors():
         Q.qat_kv_append(q, q, *meta, cache[0], cache[0], *cache[2:])
     with pytest.raises(ValueError, match="cu must have shape"):
         Q.qat_kv_attn(q, meta[0][:1], *meta[1:], *cache, q, 0.1)
+
+
+@pytest.mark.skipif(_hipcc() is None, reason="hipcc not available")
+def test_mx_tiles_wait_before_reading_accumulators():
+    # the tiled product issues its MFMAs from inline asm, like the bf16 GEMM
+    asm = _device_asm("qat_mx.hip")
+    assert asm.count("k_mx_tile") and asm.count("v_mfma_scale_f32_16x16x128_f8f6f4 a[") > 500
+    assert not accumulator_hazards(asm)

@@ -271,14 +271,11 @@ struct ReorderArgs {
   int nblk, nss;
 };
 
-__global__ __launch_bounds__(256) void k_mx_reorder(const ReorderArgs a) {
-  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int which = i >= a.n0;
-  if (which) i -= a.n0;
-  if (i >= (which ? a.n1 : a.n0)) return;
-  const int64_t row = i / a.nss;
-  const int b0 = (int)(i - row * a.nss) * 16, n = min(a.nblk - b0, 16);
-  const uint8_t* p = a.src[which] + row * a.nblk + b0;
+// 16-byte piece i of one operand.
+__device__ __forceinline__ void reorder_piece(const uint8_t* src, uint8_t* dst, int64_t i, int nblk, int nss) {
+  const int64_t row = i / nss;
+  const int b0 = (int)(i - row * nss) * 16, n = min(nblk - b0, 16);
+  const uint8_t* p = src + row * nblk + b0;
   uint32_t w[4] = {0, 0, 0, 0};
   if (n == 16) {
     __builtin_memcpy(w, p, 16);
@@ -287,7 +284,45 @@ __global__ __launch_bounds__(256) void k_mx_reorder(const ReorderArgs a) {
     for (int k = 0; k < 16; ++k)
       if (k < n) w[k >> 2] |= (uint32_t)p[k] << (8 * (k & 3));
   }
-  *(uint4*)(a.dst[which] + i * 16) = transpose4(w[0], w[1], w[2], w[3]);
+  *(uint4*)(dst + i * 16) = transpose4(w[0], w[1], w[2], w[3]);
+}
+
+__global__ __launch_bounds__(256) void k_mx_reorder(const ReorderArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < a.n0) reorder_piece(a.src[0], a.dst[0], i, a.nblk, a.nss);
+  else if (i < a.n0 + a.n1) reorder_piece(a.src[1], a.dst[1], i - a.n0, a.nblk, a.nss);
+}
+
+// qat_mx_linear before the tiled product, one launch: the first x_blocks
+// workgroups quantise X and write its scales in the tiled order (a thread has 8
+// elements, rows padded to 512), the others reorder W's.
+struct PrepareArgs {
+  const void* X;
+  int64_t ldx, x_chunks;           // rows * nss * 64
+  int x_blocks, cols;
+  uint8_t* codes;
+  ReorderArgs r;
+};
+
+template <int DT>
+__global__ __launch_bounds__(256) void k_mx_prepare(const PrepareArgs a) {
+  if ((int)blockIdx.x >= a.x_blocks) {
+    const int64_t i = (int64_t)((int)blockIdx.x - a.x_blocks) * 256 + threadIdx.x;
+    if (i < a.r.n1) reorder_piece(a.r.src[1], a.r.dst[1], i, a.r.nblk, a.r.nss);
+    return;
+  }
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.x_chunks) return;                           // a multiple of 64: whole waves
+  const int64_t piece = i >> 6, row = piece / a.r.nss;
+  const int c = (int)(i & 63), col = (int)(piece - row * a.r.nss) * 512 + c * 8;
+  uint32_t byte = 0;
+  if (col < a.cols) {                                    // the same for a block's four lanes
+    float x[8];
+    load8<DT>(a.X, row * a.ldx + col, x);
+    *(uint32_t*)(a.codes + row * (a.cols / 2) + col / 2) = quant8(x, byte);
+  }
+  const int blk = c >> 2;
+  if ((c & 3) == 0) a.r.dst[0][piece * 16 + (blk & 3) * 4 + (blk >> 2)] = (uint8_t)byte;
 }
 
 // ---------------------------------------------------------------------------
@@ -335,6 +370,14 @@ __device__ __forceinline__ void mfma_acc(f32x4& c, const i32x4& w, const i32x4& 
   else if constexpr (J == 2) QAT_MX_MFMA("op_sel_hi:[1,1,0]");
   else QAT_MX_MFMA("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
 #undef QAT_MX_MFMA
+}
+
+// dma16 (qat_dma.h) to `lds` + `imm`, the sum formed in M0.
+__device__ __forceinline__ void dma16_at(i32x4 rsrc, uint32_t lds, int imm, uint32_t voff) {
+  asm volatile("s_add_u32 m0, %0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
+               :
+               : "s"(lds), "n"(imm), "v"(voff), "s"(rsrc)
+               : "memory", "m0", "scc");
 }
 
 __device__ __forceinline__ void mfma_drain() {
@@ -412,6 +455,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_tile(const ProductArgs a
     const bool is_x = k < TM / 8;
     const int row = (is_x ? k : k - TM / 8) * 8 + r, sw = is_x ? r : (r & 3) | (row & 8) >> 1;
     vc[i] = (uint32_t)(row * ldk + (((lane & 7) ^ sw) << 4));
+    asm("" : "+v"(vc[i]));                                // kept, not formed again before each use
   }
 #pragma unroll
   for (int i = 0; i < TS::kSDma; ++i) {
@@ -423,8 +467,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_tile(const ProductArgs a
   auto issue = [&](uint32_t grp, int j, int i) {
     if (i < TS::kDma) {
       const int k = wave * TS::kDma + i;
-      dma16(k < TM / 8 ? rx : rw,
-            (uint32_t)__builtin_amdgcn_readfirstlane((int)(grp + (uint32_t)(j * TS::kStage + k * 1024))), vc[i]);
+      dma16_at(k < TM / 8 ? rx : rw, grp + (uint32_t)(wave * TS::kDma * 1024), j * TS::kStage + i * 1024, vc[i]);
     } else {
       // a wave without a share repeats the last one, so that all waves count alike
       const int k = min(wave * TS::kSDma + i - TS::kDma, TS::kRows / 64 - 1);
@@ -479,28 +522,33 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_tile(const ProductArgs a
   f32x4 acc[FN][FM];
   constexpr int NM = FM * FN, NR = FM + FN;
   static_assert(NR <= NM, "a step's reads fit its products");
-  // Step J of a group (scale byte J): product t, then a share of the DMAs (odd
-  // steps, into stage J / 2 of the group at `grp`) and, behind them, the reads of
-  // the next step (from LDS offset `off`; its scales too where a group begins).
+  // Step J of a group (scale byte J): product t, then read t of the next step
+  // (from LDS offset `off`; its scales too where a group begins) and a share of
+  // the DMAs (odd steps, into stage J / 2 of the group at `grp`). The DMAs of a
+  // CU's four waves pass its L1 at 64 bytes a cycle, a stage in 1088 of its 2048
+  // cycles: all at the step's start they stall their waves, so they are spread.
   // The fences keep this order: without them the compiler puts every read right
   // before its use.
   auto step = [&](auto jc, const Frags& cur, const Scales& sc, Frags& nxt, int off, Scales& nsc, int soff,
                   uint32_t grp) {
     constexpr int J = decltype(jc)::value;
     constexpr int ND = J % 2 == 0 ? 0 : TS::kDma + (J == 1 ? TS::kSDma : 0);
-    constexpr int kOps = ND + NR, kPer = (kOps + NM - 1) / NM;        // memory operations of a product
+    constexpr int kGap = ND > 0 && NM / ND > 1 ? NM / ND : 1;         // products from one DMA to the next
+    constexpr int kDmas = (ND + NM - 1) / NM;                         // and DMAs at a time, where there are more
+    // a read with every product (more where there are too few products for one each)
+    constexpr int kReads = (NR + NM - 1) / NM;
 #pragma unroll
     for (int t = 0; t < NM; ++t) {
       const int j = t / FM, i = t % FM;
       mfma_acc<J>(acc[j][i], cur.w[j], cur.x[i], sc.w[j], sc.x[i]);
+      if (t % kGap == 0) {
 #pragma unroll
-      for (int o = t * kPer; o < (t + 1) * kPer && o < kOps; ++o) {
-        if (o < ND) {
-          issue(grp, J / 2, o);
-        } else {
-          read(nxt, off, (J + 1) % 2, o - ND);
-          if constexpr (J == 3) read_scale(nsc, soff, o - ND);
-        }
+        for (int d = t / kGap * kDmas; d < (t / kGap + 1) * kDmas && d < ND; ++d) issue(grp, J / 2, d);
+      }
+#pragma unroll
+      for (int r = t * kReads; r < (t + 1) * kReads && r < NR; ++r) {
+        read(nxt, off, (J + 1) % 2, r);
+        if constexpr (J == 3) read_scale(nsc, soff, r);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -526,6 +574,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_tile(const ProductArgs a
   int ahead = 0, ahead_ss = 0;                            // tile and group at which the buffers stand
   auto next_group = [&]() {
     if (++ahead_ss == SS) {
+      asm volatile("");                                   // a branch: not computed and selected every time
       ahead_ss = 0;
       open(++ahead);
     }
@@ -623,8 +672,15 @@ int num_cus() {
   return cached[dev];
 }
 
-// The product takes the tiled kernel from this many tokens on.
-constexpr int64_t kTileTokens = 128;
+// Whether a product takes the tiled kernel. The other one reads its operands in
+// place, which spares the scales' reordering, but reads the weights again for
+// every 16 tokens: measured at 2.7 us for each 2^20 of (token tiles x weight
+// tiles x in), against 14 to 15 us in all for the smallest tiled products of
+// 4096 and more (32 x 4096 x 4096: 6 us against 14; 32 x 11008 x 4096: 15
+// against 15; 128 x 4096 x 4096: 20 against 14).
+bool tiled(int64_t M, int64_t out, int64_t in) {
+  return M > 16 && (M + 15) / 16 * ((out + 15) / 16) * in > (int64_t(11) << 19);
+}
 
 template <int DT, int TM, int TN, int WM, int WN, int NG>
 void launch_tile(const ProductArgs& a, hipStream_t st) {
@@ -637,49 +693,100 @@ void launch_tile(const ProductArgs& a, hipStream_t st) {
              dim3(64 * TS::kWaves), TS::kLds, st, a);
 }
 
-// Workspace: X's codes and scales (qat_mx_linear), and both operands' scales in
-// the tiled kernel's order.
+// Tile by how many there are for the chip (measured on 256 CUs, us, 64 x 64 /
+// 128 x 128 one group / two groups / 256 x 256):
+//   256 x 4096 x 4096       64 tiles of 128^2   11 / 16 / 15 / 29
+//   1024 x 4096 x 4096     256                  23 / 18 / 17 / 30
+//   2048 x 4096 x 11008    512                  97 / 55 / 57 / 67
+//   4096 x 8192 x 8192    2048                 283 / 148 / 165 / 123
+template <int DT>
+void launch_tiles(const ProductArgs& a, hipStream_t st) {
+  auto tiles = [&](int64_t t) { return (a.M + t - 1) / t * ((a.N + t - 1) / t); };
+  const int cus = num_cus();
+  if (tiles(256) >= cus) launch_tile<DT, 256, 256, 2, 2, 1>(a, st);
+  else if (tiles(128) > cus) launch_tile<DT, 128, 128, 2, 2, 1>(a, st);        // two workgroups a CU
+  else if (2 * tiles(128) > cus) launch_tile<DT, 128, 128, 2, 2, 2>(a, st);    // one: twice the depth
+  else launch_tile<DT, 64, 64, 2, 2, 2>(a, st);
+}
+
+// Workspace: X's codes (qat_mx_linear), then both operands' scales in the tiled
+// kernel's order, or X's as they are for the other one.
 struct MxWs {
-  size_t xs, xr, wr, bytes;
+  size_t xs, ws, bytes;
   static MxWs of(int64_t M, int64_t out, int64_t in, bool linear) {
     auto up = [](int64_t v) { return (size_t)((v + 255) / 256 * 256); };
     const int64_t row = (in + 511) / 512 * 16;
-    const bool tile = M > kTileTokens;
+    const bool tile = tiled(M, out, in);
     MxWs w;
     w.xs = linear ? up(M * in / 2) : 0;
-    w.xr = w.xs + (linear ? up(M * in / 32) : 0);
-    w.wr = w.xr + (tile ? up(M * row) : 0);
-    w.bytes = w.wr + (tile ? up(out * row) : 0);
+    w.ws = w.xs + (tile ? up(M * row) : linear ? up(M * in / 32) : 0);
+    w.bytes = w.ws + (tile ? up(out * row) : 0);
     return w;
   }
 };
 
-void launch_product(ProductArgs a, int dtype, uint8_t* ws, const MxWs& w, hipStream_t st) {
-  if (a.M > kTileTokens) {
-    ReorderArgs r;
-    r.nblk = a.K / 32;
-    r.nss = (r.nblk + 15) / 16;
-    r.src[0] = a.xs;
-    r.src[1] = a.ws;
-    r.dst[0] = ws + w.xr;
-    r.dst[1] = ws + w.wr;
-    r.n0 = (int64_t)a.M * r.nss;
-    r.n1 = (int64_t)a.N * r.nss;
+ReorderArgs reorder_args(const ProductArgs& a, uint8_t* ws, const MxWs& w) {
+  ReorderArgs r;
+  r.nblk = a.K / 32;
+  r.nss = (r.nblk + 15) / 16;
+  r.src[0] = a.xs;
+  r.src[1] = a.ws;
+  r.dst[0] = ws + w.xs;
+  r.dst[1] = ws + w.ws;
+  r.n0 = (int64_t)a.M * r.nss;
+  r.n1 = (int64_t)a.N * r.nss;
+  return r;
+}
+
+// The product proper: `a` has tiled scales where tiled() says so.
+void launch_product(const ProductArgs& a, int dtype, hipStream_t st) {
+  LaunchTimer t("mx_gemm", st);
+  if (tiled(a.M, a.N, a.K)) {
+    if (dtype == QAT_BF16) launch_tiles<QAT_BF16>(a, st);
+    else launch_tiles<QAT_F16>(a, st);
+    return;
+  }
+  const dim3 grid((a.N + 15) / 16, (a.M + 15) / 16);
+  if (dtype == QAT_BF16) QAT_LAUNCH(k_mx_skinny<QAT_BF16>, grid, dim3(512), 0, st, a);
+  else QAT_LAUNCH(k_mx_skinny<QAT_F16>, grid, dim3(512), 0, st, a);
+}
+
+void launch_gemm(ProductArgs a, int dtype, uint8_t* ws, const MxWs& w, hipStream_t st) {
+  if (tiled(a.M, a.N, a.K)) {
+    const ReorderArgs r = reorder_args(a, ws, w);
     {
       LaunchTimer t("mx_reorder", st);
       QAT_LAUNCH(k_mx_reorder, dim3((unsigned)((r.n0 + r.n1 + 255) / 256)), dim3(256), 0, st, r);
     }
     a.xs = r.dst[0];
     a.ws = r.dst[1];
-    LaunchTimer t("mx_gemm", st);
-    if (dtype == QAT_BF16) launch_tile<QAT_BF16, 256, 256, 2, 2, 1>(a, st);
-    else launch_tile<QAT_F16, 256, 256, 2, 2, 1>(a, st);
-    return;
   }
-  LaunchTimer t("mx_gemm", st);
-  const dim3 grid((a.N + 15) / 16, (a.M + 15) / 16);
-  if (dtype == QAT_BF16) QAT_LAUNCH(k_mx_skinny<QAT_BF16>, grid, dim3(512), 0, st, a);
-  else QAT_LAUNCH(k_mx_skinny<QAT_F16>, grid, dim3(512), 0, st, a);
+  launch_product(a, dtype, st);
+}
+
+void launch_linear(const void* X, int64_t ldx, ProductArgs a, int dtype, uint8_t* ws, const MxWs& w, hipStream_t st) {
+  a.xc = ws;
+  a.xs = ws + w.xs;
+  if (tiled(a.M, a.N, a.K)) {
+    PrepareArgs p;
+    p.X = X;
+    p.ldx = ldx;
+    p.cols = a.K;
+    p.codes = ws;
+    p.r = reorder_args(a, ws, w);
+    p.x_chunks = p.r.n0 * 64;
+    p.x_blocks = (int)((p.x_chunks + 255) / 256);
+    {
+      LaunchTimer t("mx_prepare", st);
+      const dim3 grid((unsigned)(p.x_blocks + (p.r.n1 + 255) / 256));
+      if (dtype == QAT_BF16) QAT_LAUNCH(k_mx_prepare<QAT_BF16>, grid, dim3(256), 0, st, p);
+      else QAT_LAUNCH(k_mx_prepare<QAT_F16>, grid, dim3(256), 0, st, p);
+    }
+    a.ws = p.r.dst[1];
+  } else {
+    launch_quant(X, dtype, a.M, a.K, ldx, ws, ws + w.xs, nullptr, st);
+  }
+  launch_product(a, dtype, st);
 }
 
 int32_t check_product(int64_t M, int64_t out, int64_t in, int32_t dtype, int64_t ldy) {
@@ -733,7 +840,7 @@ QAT_API int32_t qat_mx_gemm(const uint8_t* X_codes, const uint8_t* X_scales, con
                         {{X_codes, (size_t)(M * in / 2)}, {X_scales, (size_t)(M * in / 32)},
                          {W_codes, (size_t)(out * in / 2)}, {W_scales, (size_t)(out * in / 32)}}));
   ProductArgs a{X_codes, X_scales, W_codes, W_scales, (int)M, (int)out, (int)in, Y, ldy};
-  launch_product(a, dtype, (uint8_t*)ws, w, stream);
+  launch_gemm(a, dtype, (uint8_t*)ws, w, stream);
   return finish_call();
 }
 
@@ -752,10 +859,7 @@ QAT_API int32_t qat_mx_linear(const void* X, int64_t ldx, const uint8_t* W_codes
   QAT_CHECK(check_spans({{Y, strided_bytes(M, ldy, out, 2)}, {ws, w.bytes}},
                         {{X, strided_bytes(M, ldx, in, 2)}, {W_codes, (size_t)(out * in / 2)},
                          {W_scales, (size_t)(out * in / 32)}}));
-  uint8_t* xc = (uint8_t*)ws;
-  uint8_t* xs = xc + w.xs;
-  launch_quant(X, dtype, M, in, ldx, xc, xs, nullptr, stream);
-  ProductArgs a{xc, xs, W_codes, W_scales, (int)M, (int)out, (int)in, Y, ldy};
-  launch_product(a, dtype, (uint8_t*)ws, w, stream);
+  ProductArgs a{nullptr, nullptr, W_codes, W_scales, (int)M, (int)out, (int)in, Y, ldy};
+  launch_linear(X, ldx, a, dtype, (uint8_t*)ws, w, stream);
   return finish_call();
 }
