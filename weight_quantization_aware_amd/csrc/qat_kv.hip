@@ -2,6 +2,8 @@
 // paged 8-bit cache of keys and values, and the attention that reads it.
 #include <math.h>
 
+#include <type_traits>
+
 #include "../../include/qat_kv.h"
 #include "qat_check.h"
 #include "qat_device.h"
@@ -308,11 +310,12 @@ __global__ __launch_bounds__(NT) void k_kv_append(const AppendArgs a) {
 //   O^T += V^T P^T: the lane's 16 probabilities are the B operand as they sit;
 //     the A operand, d = 16 jd + r16 and the same 16 positions, is 16
 //     consecutive bytes of the cache's [d][token] value block.
-// The softmax runs with a lazily moved row maximum in base 2. A probability is
-// multiplied by its page's value scale over a reference (the largest so far)
-// and rounded to fp16: 11 bits, against bf16's 8, and e4m3 is exact in fp16.
-// The product of the two is at most 2^12; what falls below fp16's 2^-24 is
-// 2^-24 of the largest weight of the row.
+// The softmax runs with a lazily moved row maximum in base 2; a lane asks with
+// its own positions' maximum whether it has to move, and the lanes of a row
+// join theirs only then. A probability is multiplied by its page's value scale
+// over a reference (the largest so far) and rounded to fp16: 11 bits, against
+// bf16's 8, and e4m3 is exact in fp16. The product of the two is at most 2^12;
+// what falls below fp16's 2^-24 is 2^-24 of the largest weight of the row.
 // ---------------------------------------------------------------------------
 struct AttnArgs {
   const uint16_t* q;
@@ -333,6 +336,7 @@ struct AttnArgs {
   int64_t ldo;
   int target;                      // work items a key head should have in all; 0: one item a sequence
   int max_rows;                    // max_new * group
+  int row_blocks;                  // of a sequence and key head (prompts)
   float* part_o;                   // [item][key head][max_rows][head_dim]
   float* part_ml;                  // [item][key head][max_rows][2]
 };
@@ -341,6 +345,7 @@ constexpr int kTile = 64;          // positions of a block
 constexpr int kMinTiles = 8;       // blocks of a work item at least: two for each of its four waves
 constexpr float kLazy = 8.0f;      // how far (log2) a block's maximum may pass the subtracted one
 constexpr float kLazyV = 4.0f;     // the same of value scales over their reference
+constexpr float kLowC = -40.0f;    // log2 of a value scale over the reference is held at this or more
 
 struct Seq {
   int64_t c0;                      // first new token
@@ -409,6 +414,12 @@ __device__ __forceinline__ bool find_item(const AttnArgs& a, int item, int chunk
   return false;
 }
 
+// Largest value over the four lanes that share lane & 15.
+__device__ __forceinline__ float max_over_g(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+
 // 8 codes (two dwords) as bf16 or fp16.
 template <int DT>
 __device__ __forceinline__ typename Half8<DT>::v codes8(uint32_t lo, uint32_t hi) {
@@ -432,6 +443,43 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
 }
 __device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Takes the values that are not numbers out of 8 fp16 values (zero in their
+// place) and returns 1 for each of them, 0 for the others. On the bits, two at
+// a time: compared one by one, the 128 truth values of a block would not fit
+// the scalar registers.
+__device__ __forceinline__ f16x8 take_nan(f16x8& v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 u = __builtin_bit_cast(u32x4, v), n;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    // above 0x7C00 without the sign: the sum carries into bit 15
+    const uint32_t top = ((u[j] & 0x7FFF7FFFu) + 0x03FF03FFu) & 0x80008000u;
+    const uint32_t mask = (top >> 15) * 0xFFFFu;
+    u[j] &= ~mask;
+    n[j] = mask & 0x3C003C00u;
+  }
+  v = __builtin_bit_cast(f16x8, u);
+  return __builtin_bit_cast(f16x8, n);
+}
+
+// 1 for the first `n` of 8 fp16 values, 0 for the others.
+__device__ __forceinline__ f16x8 ones8(int n) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int k = min(max(n - 2 * j, 0), 2);
+    u[j] = 0x3C003C00u & (uint32_t)((1ull << (16 * k)) - 1);
+  }
+  return __builtin_bit_cast(f16x8, u);
+}
+
+// Whether one of 16 codes is not a number.
+__device__ __forceinline__ bool has_nan(uint4 u) {
+  const uint32_t k7 = 0x7F7F7F7Fu, k1 = 0x01010101u;
+  return ((((u.x & k7) + k1) | ((u.y & k7) + k1) | ((u.z & k7) + k1) | ((u.w & k7) + k1)) & 0x80808080u) != 0;
 }
 
 // The first `n` (0 .. 16) bytes of 16, the others zero.
@@ -539,7 +587,7 @@ __global__ __launch_bounds__(256, 2) void k_kv_decode(const AttnArgs a) {
   };
 
   f32x4 o[RT][JD];
-  float m[RT], l[RT];
+  float m[RT], l[RT];                                    // l: this lane's share of the row's sum
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     m[i] = -INFINITY;
@@ -566,38 +614,38 @@ __global__ __launch_bounds__(256, 2) void k_kv_decode(const AttnArgs a) {
       }
     }
     if (more) load_k(t + 4);
-    const float f = xks * a.scale_log2;
+    // positive, so that the maximum can be taken before it, and never zero, so
+    // that a masked score stays -inf
+    const float f = fmaxf(xks * a.scale_log2, 0x1p-126f);
     const int key0 = 64 * t + 16 * g;
     float mx[RT];
     bool grow = false;
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      float y = -INFINITY;
-      const int seen = min(lim[i] - key0, have);       // of the lane's 16 positions
+      if (edge) {
+        const int seen = min(lim[i] - key0, have);       // of the lane's 16 positions
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (4 * jt + r >= seen) sc[i][jt][r] = -INFINITY;
+      }
+      float y = sc[i][0][0];
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float v = sc[i][jt][r] * f;
-          if (edge && 4 * jt + r >= seen) v = -INFINITY;
-          sc[i][jt][r] = v;
-          y = fmaxf(y, v);
-        }
-      y = fmaxf(y, __shfl_xor(y, 16));
-      mx[i] = fmaxf(y, __shfl_xor(y, 32));
+        for (int r = 0; r < 4; ++r) y = fmaxf(y, sc[i][jt][r]);
+      mx[i] = y * f;                                     // of the lane's positions: enough to ask
       grow = grow || mx[i] > m[i] + kLazy;
     }
     const float lv = have > 0 ? __builtin_amdgcn_logf(xvs) : -INFINITY;
-    float lvm = fmaxf(lv, __shfl_xor(lv, 16));
-    lvm = fmaxf(lvm, __shfl_xor(lvm, 32));
-    const bool grow_v = lvm > vref + kLazyV;
-    if (__any(grow || grow_v)) {
-      const float vn = grow_v ? lvm : vref;
+    if (__any(grow || lv > vref + kLazyV)) {
+      const float lvm = max_over_g(lv), vn = lvm > vref + kLazyV ? lvm : vref;
       const float fv = vref == vn ? 1.0f : __builtin_amdgcn_exp2f(vref - vn);
       vref = vn;
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        const float mn = fmaxf(m[i], mx[i]);
+        const float mn = fmaxf(m[i], max_over_g(mx[i]));
         const float al = m[i] == mn ? 1.0f : __builtin_amdgcn_exp2f(m[i] - mn);
         l[i] *= al;
         m[i] = mn;
@@ -607,23 +655,25 @@ __global__ __launch_bounds__(256, 2) void k_kv_decode(const AttnArgs a) {
           for (int r = 0; r < 4; ++r) o[i][jd][r] *= al * fv;
       }
     }
-    const float c = have > 0 ? __builtin_amdgcn_exp2f(lv - vref) : 0.0f;
+    // w = 2^(s f + log2 c - m), c the lane's value scale over the reference; the
+    // softmax's sum takes 1 / c once for the lane's 16 positions
+    const float lc = have > 0 ? fmaxf(lv - vref, kLowC) : 0.0f;
+    const float rc = __builtin_amdgcn_exp2f(-lc);
     f16x8 pf[RT][2];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       // a row that has seen nothing yet has m = -inf: its scores are all -inf
-      const float ms = m[i] == -INFINITY ? 0.0f : m[i];
+      const float ms = lc - (m[i] == -INFINITY ? 0.0f : m[i]);
       float sum = 0.f;
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float p = __builtin_amdgcn_exp2f(sc[i][jt][r] - ms);
-          sum += p;
-          pf[i][jt >> 1][4 * (jt & 1) + r] = (_Float16)(p * c);
+          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i][jt][r], f, ms));
+          sum += w;
+          pf[i][jt >> 1][4 * (jt & 1) + r] = (_Float16)w;
         }
-      sum += __shfl_xor(sum, 16);
-      l[i] += sum + __shfl_xor(sum, 32);
+      l[i] += sum * rc;
     }
     if (!edge) {
 #pragma unroll
@@ -637,33 +687,19 @@ __global__ __launch_bounds__(256, 2) void k_kv_decode(const AttnArgs a) {
       // limits differ, a value that is not a number may be seen by one row and
       // masked for another: it is taken out of the product, and counted apart
       // against the positions that each row sees.
-      f16x8 one[RT][2];
-      if (!one_limit) {
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int k = 0; k < 16; ++k) one[i][k >> 3][k & 7] = (_Float16)(k < min(lim[i] - key0, have) ? 1.f : 0.f);
-      }
       const int keep = one_limit ? min(lo_lim - key0, have) : have;
 #pragma unroll
       for (int jd = 0; jd < JD; ++jd) {
         const uint4 u = first_bytes(xv[jd], keep);
         f16x8 v0 = codes8<QAT_F16>(u.x, u.y), v1 = codes8<QAT_F16>(u.z, u.w);
         if (!one_limit) {
-          f16x8 n0, n1;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            n0[k] = (_Float16)(v0[k] == v0[k] ? 0.f : 1.f);
-            n1[k] = (_Float16)(v1[k] == v1[k] ? 0.f : 1.f);
-            v0[k] = v0[k] == v0[k] ? v0[k] : (_Float16)0.f;
-            v1[k] = v1[k] == v1[k] ? v1[k] : (_Float16)0.f;
-          }
+          const f16x8 n0 = take_nan(v0), n1 = take_nan(v1);
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
-            const f32x4 cnt = mfma16(n1, one[i][1], mfma16(n0, one[i][0], f32x4{0.f, 0.f, 0.f, 0.f}));
+            const int seen = min(lim[i] - key0, have);
+            const f32x4 cnt = mfma16(n1, ones8(seen - 8), mfma16(n0, ones8(seen), f32x4{0.f, 0.f, 0.f, 0.f}));
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (cnt[r] > 0.f) o[i][jd][r] = NAN;
+            for (int r = 0; r < 4; ++r) o[i][jd][r] = cnt[r] > 0.f ? NAN : o[i][jd][r];
           }
         }
 #pragma unroll
@@ -702,9 +738,12 @@ __global__ __launch_bounds__(256, 2) void k_kv_decode(const AttnArgs a) {
       const f32x4 v = o[i][jd];
       *(f32x4*)&so[wave][r16][16 * jd + 4 * g] = f32x4{v[0] * vscale, v[1] * vscale, v[2] * vscale, v[3] * vscale};
     }
+    float row_sum = l[i];
+    row_sum += __shfl_xor(row_sum, 16);
+    row_sum += __shfl_xor(row_sum, 32);
     if (g == 0) {
       sm[wave][r16] = m[i];
-      sl[wave][r16] = l[i];
+      sl[wave][r16] = row_sum;
     }
     __syncthreads();
     const int rr = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * (D / 16);
@@ -736,6 +775,361 @@ __global__ __launch_bounds__(256, 2) void k_kv_decode(const AttnArgs a) {
       for (int j = 0; j < D / 16; j += 4)
         *(f32x4*)(a.part_o + at * D + d0 + j) = f32x4{acc[j], acc[j + 1], acc[j + 2], acc[j + 3]};
       if (d0 == 0) *(f32x2*)(a.part_ml + at * 2) = f32x2{mm, ll};
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Attention over the cache, many rows (prompts). A workgroup of four waves owns
+// 64 RT rows of one (sequence, key head), 16 RT a wave, and visits the blocks of
+// 64 positions that they see. A block's codes are made 16-bit once for all rows
+// and put into LDS (two buffers; the next block's codes are in flight in
+// registers during this one's products); the products and the layout of a
+// lane's scores are those of k_kv_decode. Bound by the matrix cores and, close
+// behind, by the softmax's vector work, which is kept to a maximum, an FMA, an
+// exponential and a sum for each score: the row maximum and both page scales
+// are one FMA's constants. (A page's value scale over the reference is held at
+// 2^-40 or more: below that the fp16 weights are zero either way.)
+//
+// LDS: keys [64][D], 16-byte chunk c of key k at c ^ (k & 3 | k >> 2 & 12)
+// (for D = 64, 8 chunks, at the lowest three bits of that with k & 4's), values
+// [D][64], chunk c of row d at c ^ (d & 7): fragment reads use every bank
+// equally.
+// ---------------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ int key_chunk(int key, int c) {
+  const int sw = (key & 3) | (key >> 2 & 12);
+  return D == 128 ? c ^ sw : c ^ (sw & 7);
+}
+
+template <int DT, int D, int RT>
+__global__ __launch_bounds__(256, RT == 2 ? 2 : 1) void k_kv_prompt(const AttnArgs a) {
+  typedef typename Half8<DT>::v half8;
+  constexpr int JD = D / 16, KS = D / 32, kRows = 64 * RT;
+  constexpr int kBuf = 64 * D * 2;                       // bytes of one operand's block
+  constexpr int NP = D / 64;                             // 16-byte pieces of a thread, each operand
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2][2][kBuf];   // [buffer][keys, values]
+  // values that are not numbers (rare): whether wave w put one, and where: bit j
+  // of row d for position j, written by the rows' wave when it did
+  __shared__ __attribute__((aligned(16))) int nan_of[2][4];
+  __shared__ __attribute__((aligned(8))) uint16_t nan_at[2][D][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  // (row block, sequence and head): the blocks of one head on one XCD where the
+  // heads are a multiple of 8, the longest (last) blocks first
+  const int nrb = a.row_blocks, w = blockIdx.x;
+  int prob = w / nrb, rb = nrb - 1 - (w - prob * nrb);
+  if ((a.batch * a.hk & 7) == 0) {
+    const int r = w % (8 * nrb);
+    prob = 8 * (w / (8 * nrb)) + (r & 7);
+    rb = nrb - 1 - (r >> 3);
+  }
+  const int b = prob / a.hk, h = prob - b * a.hk;
+  const Seq s = seq_of(a, b);
+  const int rows = s.n * a.group, row_base = rb * kRows;
+  if (row_base >= rows) return;
+
+  // this lane's rows (16 i + r16 of its wave's), their limits and queries
+  half8 qf[RT][KS];
+  int lim[RT], lo_lim = 0x7FFFFFFF, hi_lim = 0;
+  const int wave_base = row_base + wave * 16 * RT;
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int rc = min(wave_base + 16 * i + r16, rows - 1);
+    const int tok = rc / a.group, hh = rc - tok * a.group;
+    const int64_t seen = a.causal ? s.start + tok + 1 : (int64_t)s.len;
+    lim[i] = (int)max(min(seen, (int64_t)s.len), (int64_t)0);
+    lo_lim = min(lo_lim, lim[i]);
+    hi_lim = max(hi_lim, lim[i]);
+    const uint16_t* qp = a.q + (s.c0 + tok) * a.ldq + (int64_t)(h * a.group + hh) * D + 8 * g;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) qf[i][ks] = *(const half8*)(qp + 32 * ks);
+  }
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    lo_lim = min(lo_lim, __shfl_xor(lo_lim, o));
+    hi_lim = max(hi_lim, __shfl_xor(hi_lim, o));
+  }
+  lo_lim = __builtin_amdgcn_readfirstlane(lo_lim);
+  hi_lim = __builtin_amdgcn_readfirstlane(hi_lim);       // of the wave
+  // limits grow with the row: the workgroup's last row sees most
+  const int last_tok = (min(row_base + kRows, rows) - 1) / a.group;
+  const int64_t most = a.causal ? min(s.start + last_tok + 1, (int64_t)s.len) : (int64_t)s.len;
+  const int tiles = (int)((max(most, (int64_t)0) + kTile - 1) / kTile);
+
+  const int32_t* table = a.table + b * a.cols;
+  const int page = 1 << a.log_page, last16 = max(s.len - 1, 0) >> 4;
+  const int64_t head_bytes = (int64_t)page * D;
+  auto page_of = [&](int t, int sub) { return table[(min(4 * t + sub, last16) << 4) >> a.log_page]; };
+  auto block_of = [&](int id, bool& bad) {
+    bad = (uint32_t)id >= (uint64_t)a.n_pages;
+    return (int64_t)(bad ? 0 : id) * a.hk + h;
+  };
+
+  // Staging: piece p = i * 256 + tid is 16 codes: keys' d 16 (p % (D / 16)) .. of
+  // key p / (D / 16), and values' positions 16 (p % 4) .. of row d = p / 4.
+  uint4 rk[NP], rv[NP];
+  float nks = 0.f, nvs = 0.f;                            // the lane's 16 positions' scales, of the block in flight
+  int nhave = 0, nkeep = 0;
+  // Page ids are fetched a block ahead of the loads that need them.
+  int id_k[NP], id_v, id_s;
+  auto load_ids = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) id_k[i] = page_of(t, (i * 256 + tid) / JD >> 4);
+    id_v = page_of(t, tid & 3);
+    id_s = page_of(t, g);
+  };
+  auto load = [&](int t) {
+    bool bad;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int p = i * 256 + tid, key = p / JD;
+      const int64_t blk = block_of(id_k[i], bad);
+      const int slot = ((min(4 * t + (key >> 4), last16) << 4) & (page - 1)) + (key & 15);
+      rk[i] = *(const uint4*)(a.k + blk * head_bytes + (int64_t)slot * D + (p % JD) * 16);
+    }
+    const int sub = tid & 3;                             // of the thread's values: 256 is a multiple of 4
+    const int64_t blk = block_of(id_v, bad);
+    const uint8_t* vp = a.v + blk * head_bytes + ((min(4 * t + sub, last16) << 4) & (page - 1));
+    nkeep = bad ? 0 : s.len - 64 * t - 16 * sub;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) rv[i] = *(const uint4*)(vp + (i * 64 + (tid >> 2)) * page);
+    const int64_t bg = block_of(id_s, bad);
+    nks = a.ks[bg];
+    nvs = a.vs[bg];
+    nhave = bad ? 0 : min(max(s.len - 64 * t - 16 * g, 0), 16);
+  };
+  auto put = [&](int buf) {
+    bool nan = false;
+    if (__any(nkeep < 16)) {                             // absent positions' values are zero whatever they hold
+#pragma unroll
+      for (int i = 0; i < NP; ++i) rv[i] = first_bytes(rv[i], nkeep);
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) nan = nan || has_nan(rv[i]);
+    const bool any = __any(nan);
+    if (lane == 0) nan_of[buf][wave] = any;
+    if (any) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        uint32_t u[4] = {rv[i].x, rv[i].y, rv[i].z, rv[i].w}, at = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t top = ((u[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+          u[j] &= ~((top >> 7) * 255u);
+          at |= (((top >> 7) * 0x01020408u) >> 24 & 15u) << (4 * j);
+        }
+        rv[i] = make_uint4(u[0], u[1], u[2], u[3]);
+        nan_at[buf][i * 64 + (tid >> 2)][tid & 3] = (uint16_t)at;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int p = i * 256 + tid, key = p / JD, c = (p % JD) * 2;
+      uint8_t* kr = smem[buf][0] + key * (2 * D);
+      *(half8*)(kr + key_chunk<D>(key, c) * 16) = codes8<DT>(rk[i].x, rk[i].y);
+      *(half8*)(kr + key_chunk<D>(key, c + 1) * 16) = codes8<DT>(rk[i].z, rk[i].w);
+      const int d = p >> 2, cv = (p & 3) * 2;
+      uint8_t* vr = smem[buf][1] + d * 128;
+      *(f16x8*)(vr + ((cv ^ (d & 7)) << 4)) = codes8<QAT_F16>(rv[i].x, rv[i].y);
+      *(f16x8*)(vr + (((cv + 1) ^ (d & 7)) << 4)) = codes8<QAT_F16>(rv[i].z, rv[i].w);
+    }
+  };
+
+  // fragment offsets: key 16 (r16 / 4) + 4 jt + r16 % 4, chunk 4 ks + g; value row 16 jd + r16, chunk 2 g + k2
+  int koff[KS], voff[2];
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) {
+    const int key = 16 * (r16 >> 2) + (r16 & 3);
+    koff[ks] = key * (2 * D) + key_chunk<D>(key, 4 * ks + g) * 16;
+  }
+#pragma unroll
+  for (int k2 = 0; k2 < 2; ++k2) voff[k2] = r16 * 128 + (((2 * g + k2) ^ (r16 & 7)) << 4);
+
+  f32x4 o[RT][JD];
+  float m[RT], l[RT];                                    // l: this lane's share of the row's sum
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int jd = 0; jd < JD; ++jd) o[i][jd] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  float vref = -INFINITY;
+
+  uint32_t nan_out[RT];                                  // bit 4 jd + r: output d = 16 jd + 4 g + r is NaN
+#pragma unroll
+  for (int i = 0; i < RT; ++i) nan_out[i] = 0;
+  auto compute = [&](int t, int buf, float kscale, float vscale, int have) {
+    // some position of the block is masked for some row, absent, or in a page left out
+    const bool edge = 64 * t + 64 > lo_lim || __any(have < 16);
+    const int key0 = 64 * t + 16 * g;
+    f32x4 sc[RT][4];
+    // fragments of a key tile are read one tile ahead; the fences keep the
+    // compiler from reading all of them at once, which spills
+    const uint8_t* kr = smem[buf][0];
+    half8 kf[2][KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) kf[0][ks] = *(const half8*)(kr + koff[ks]);
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+      if (jt < 3) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) kf[(jt + 1) & 1][ks] = *(const half8*)(kr + koff[ks] + (jt + 1) * 8 * D);
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i) sc[i][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) sc[i][jt] = mfma16(kf[jt & 1][ks], qf[i][ks], sc[i][jt]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // positive, so that the maximum can be taken before it, and never zero, so
+    // that a masked score stays -inf
+    const float f = fmaxf(kscale * a.scale_log2, 0x1p-126f);
+    float mx[RT];
+    bool grow = false;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      if (edge) {
+        const int seen = min(lim[i] - key0, have);       // of the lane's 16 positions
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (4 * jt + r >= seen) sc[i][jt][r] = -INFINITY;
+      }
+      float y = sc[i][0][0];
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y = fmaxf(y, sc[i][jt][r]);
+      mx[i] = y * f;                                     // of the lane's positions: enough to ask
+      grow = grow || mx[i] > m[i] + kLazy;
+    }
+    const float lv = have > 0 ? __builtin_amdgcn_logf(vscale) : -INFINITY;
+    if (__any(grow || lv > vref + kLazyV)) {
+      const float lvm = max_over_g(lv), vn = lvm > vref + kLazyV ? lvm : vref;
+      const float fv = vref == vn ? 1.0f : __builtin_amdgcn_exp2f(vref - vn);
+      vref = vn;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const float mn = fmaxf(m[i], max_over_g(mx[i]));
+        const float al = m[i] == mn ? 1.0f : __builtin_amdgcn_exp2f(m[i] - mn);
+        l[i] *= al;
+        m[i] = mn;
+#pragma unroll
+        for (int jd = 0; jd < JD; ++jd)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[i][jd][r] *= al * fv;
+      }
+    }
+    const float lc = have > 0 ? fmaxf(lv - vref, kLowC) : 0.0f;
+    const float rc = __builtin_amdgcn_exp2f(-lc);
+    f16x8 pf[RT][2];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      // a row that has seen nothing yet has m = -inf: its scores are all -inf
+      const float ms = lc - (m[i] == -INFINITY ? 0.0f : m[i]);
+      float sum = 0.f;
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i][jt][r], f, ms));
+          sum += w;
+          pf[i][jt >> 1][4 * (jt & 1) + r] = (_Float16)w;
+        }
+      l[i] += sum * rc;
+    }
+    const uint8_t* vt = smem[buf][1];
+    auto vfrag = [&](int jd, int k2) { return *(const f16x8*)(vt + voff[k2] + jd * 2048); };
+    {
+      f16x8 vf[2][2];
+      vf[0][0] = vfrag(0, 0);
+      vf[0][1] = vfrag(0, 1);
+#pragma unroll
+      for (int jd = 0; jd < JD; ++jd) {
+        if (jd + 1 < JD) {
+          vf[(jd + 1) & 1][0] = vfrag(jd + 1, 0);
+          vf[(jd + 1) & 1][1] = vfrag(jd + 1, 1);
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) o[i][jd] = mfma16(vf[jd & 1][1], pf[i][1], mfma16(vf[jd & 1][0], pf[i][0], o[i][jd]));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    // Values that are not numbers were taken out of the block, since one row may
+    // see what is masked for another: a row that sees one gets NaN. Row d = 16 jd
+    // + .. was put by wave jd % 4.
+    const int4 nan = *(const int4*)nan_of[buf];
+    if (__builtin_amdgcn_readfirstlane(nan.x | nan.y | nan.z | nan.w)) {
+      const int put_by[4] = {nan.x, nan.y, nan.z, nan.w};
+      uint64_t sees[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const int n = min(max(lim[i] - 64 * t, 0), 64);
+        sees[i] = n == 64 ? ~0ull : (1ull << n) - 1;
+      }
+#pragma unroll
+      for (int jd = 0; jd < JD; ++jd) {
+        if (!__builtin_amdgcn_readfirstlane(put_by[jd & 3])) continue;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint64_t at = *(const uint64_t*)nan_at[buf][16 * jd + 4 * g + r];
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+            nan_out[i] |= at & sees[i] ? 1u << (4 * jd + r) : 0u;
+        }
+      }
+    }
+  };
+
+  if (tiles > 0) {
+    load_ids(0);
+    load(0);
+    load_ids(1);
+    put(0);
+    float ks = nks, vs = nvs;
+    int have = nhave;
+    __syncthreads();
+    for (int t = 0; t < tiles; ++t) {
+      if (t + 1 < tiles) {
+        load(t + 1);
+        load_ids(t + 2);                                 // clamped to the last positions
+      }
+      // a block that none of the wave's rows sees is passed over; the barrier is not
+      if (64 * t < hi_lim) {
+        compute(t, t & 1, ks, vs, have);
+      }
+      if (t + 1 < tiles) {
+        put((t + 1) & 1);
+        ks = nks;
+        vs = nvs;
+        have = nhave;
+      }
+      __syncthreads();
+    }
+  }
+
+  const float vscale = vref == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(vref);
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    float ll = l[i];
+    ll += __shfl_xor(ll, 16);
+    ll += __shfl_xor(ll, 32);
+    const int row = wave_base + 16 * i + r16;
+    if (row >= rows) continue;
+    const float inv = ll == 0.f ? 0.0f : vscale / ll;
+    const int tok = row / a.group, hh = row - tok * a.group;
+    uint16_t* op = a.out + (s.c0 + tok) * a.ldo + (int64_t)(h * a.group + hh) * D + 4 * g;
+#pragma unroll
+    for (int jd = 0; jd < JD; ++jd) {
+      float v[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = nan_out[i] >> (4 * jd + r) & 1 ? NAN : o[i][jd][r] * inv;
+      *(uint2*)(op + 16 * jd) = make_uint2(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]));
     }
   }
 }
@@ -797,6 +1191,7 @@ void launch_append(const AppendArgs& a, int64_t batch, hipStream_t st) {
 }
 
 struct AttnPlan {
+  bool prompt;
   int rt, row_blocks, target, items;
   size_t ml_at, bytes;             // workspace: part_o, then part_ml
 };
@@ -806,6 +1201,14 @@ constexpr int kTargetGroups = 512; // two workgroups on each of 256 CUs
 AttnPlan plan_attn(int64_t batch, int64_t hk, int64_t group, int d, int64_t max_new, int64_t max_len) {
   AttnPlan p;
   const int64_t rows = max_new * group;
+  p.prompt = rows > 32;
+  if (p.prompt) {
+    p.rt = 2;
+    p.row_blocks = (int)((rows + 64 * p.rt - 1) / (64 * p.rt));
+    p.target = p.items = 0;
+    p.ml_at = p.bytes = 0;
+    return p;
+  }
   p.rt = rows <= 16 ? 1 : 2;
   p.row_blocks = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
   const int64_t per = hk * p.row_blocks;
@@ -823,6 +1226,13 @@ AttnPlan plan_attn(int64_t batch, int64_t hk, int64_t group, int d, int64_t max_
 
 template <int DT, int D>
 void launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+  if (p.prompt) {
+    LaunchTimer t("kv_attn", st);
+    const dim3 grid((unsigned)((int64_t)p.row_blocks * a.batch * a.hk));
+    if (p.rt == 2) QAT_LAUNCH((k_kv_prompt<DT, D, 2>), grid, dim3(256), 0, st, a);
+    else QAT_LAUNCH((k_kv_prompt<DT, D, 4>), grid, dim3(256), 0, st, a);
+    return;
+  }
   {
     LaunchTimer t("kv_attn", st);
     const dim3 grid((unsigned)(a.target ? p.items : a.batch), (unsigned)a.hk, (unsigned)p.row_blocks);
@@ -1033,7 +1443,8 @@ QAT_API int32_t qat_kv_attn(const void* q, int32_t dtype, int64_t ldq, const int
   if (((uintptr_t)cu | (uintptr_t)lens | (uintptr_t)table | (uintptr_t)k_scale | (uintptr_t)v_scale) & 3)
     return QAT_ERR_ALIGN;
   const AttnPlan p = plan_attn(batch, heads_kv, heads_q / heads_kv, head_dim, mn, max_len);
-  if (p.row_blocks > kMaxGrid) return QAT_ERR_SHAPE;
+  // grids: rows of a few sequences along z, of prompts with sequences and heads along x
+  if (p.prompt ? (int64_t)p.row_blocks * batch * heads_kv > 0x7FFFFFFF : p.row_blocks > kMaxGrid) return QAT_ERR_SHAPE;
   if (p.bytes && (!ws || ws_bytes < p.bytes)) return QAT_ERR_WORKSPACE;
   const size_t nc = (size_t)(n_pages * krow * page), ns = (size_t)(n_pages * heads_kv * 4);
   QAT_CHECK(check_spans({{out, strided_bytes(tokens, ldo, row, 2)}, {ws, p.bytes}},
@@ -1065,6 +1476,7 @@ QAT_API int32_t qat_kv_attn(const void* q, int32_t dtype, int64_t ldq, const int
   a.ldo = ldo;
   a.target = p.target;
   a.max_rows = (int)(mn * a.group);
+  a.row_blocks = p.row_blocks;
   a.part_o = (float*)ws;
   a.part_ml = (float*)((uint8_t*)ws + p.ml_at);
   if (head_dim == 128) {
