@@ -345,6 +345,7 @@ constexpr int kTile = 64;          // positions of a block
 constexpr int kMinTiles = 8;       // blocks of a work item at least: two for each of its four waves
 constexpr float kLazy = 8.0f;      // how far (log2) a block's maximum may pass the subtracted one
 constexpr float kLazyV = 4.0f;     // the same of value scales over their reference
+constexpr float kMostSum = 32768.0f; // of a lane's 16 weights, each a fp16 number then
 constexpr float kLowC = -40.0f;    // log2 of a value scale over the reference is held at this or more
 
 struct Seq {
@@ -781,8 +782,8 @@ __global__ __launch_bounds__(256, 2) void k_kv_decode(const AttnArgs a) {
 
 // ---------------------------------------------------------------------------
 // Attention over the cache, many rows (prompts). A workgroup of four waves owns
-// 64 RT rows of one (sequence, key head), 16 RT a wave, and visits the blocks of
-// 64 positions that they see. A block's codes are made 16-bit once for all rows
+// 128 rows of one (sequence, key head) and visits the blocks of 64 positions
+// that they see. A block's codes are made 16-bit once for all rows
 // and put into LDS (two buffers; the next block's codes are in flight in
 // registers during this one's products); the products and the layout of a
 // lane's scores are those of k_kv_decode. Bound by the matrix cores and, close
@@ -802,16 +803,16 @@ __device__ __forceinline__ int key_chunk(int key, int c) {
   return D == 128 ? c ^ sw : c ^ (sw & 7);
 }
 
-template <int DT, int D, int RT>
-__global__ __launch_bounds__(256, RT == 2 ? 2 : 1) void k_kv_prompt(const AttnArgs a) {
+template <int DT, int D>
+__global__ __launch_bounds__(256, 2) void k_kv_prompt(const AttnArgs a) {
   typedef typename Half8<DT>::v half8;
-  constexpr int JD = D / 16, KS = D / 32, kRows = 64 * RT;
+  constexpr int NW = 4, RT = 2, JD = D / 16, KS = D / 32, kRows = 16 * RT * NW, NT = 64 * NW;
   constexpr int kBuf = 64 * D * 2;                       // bytes of one operand's block
-  constexpr int NP = D / 64;                             // 16-byte pieces of a thread, each operand
+  constexpr int NP = 4 * D / NT;                         // 16-byte pieces of a thread, each operand
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2][2][kBuf];   // [buffer][keys, values]
   // values that are not numbers (rare): whether wave w put one, and where: bit j
   // of row d for position j, written by the rows' wave when it did
-  __shared__ __attribute__((aligned(16))) int nan_of[2][4];
+  __shared__ __attribute__((aligned(16))) int nan_of[2][NW];
   __shared__ __attribute__((aligned(8))) uint16_t nan_at[2][D][4];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, g = lane >> 4;
@@ -859,15 +860,18 @@ __global__ __launch_bounds__(256, RT == 2 ? 2 : 1) void k_kv_prompt(const AttnAr
 
   const int32_t* table = a.table + b * a.cols;
   const int page = 1 << a.log_page, last16 = max(s.len - 1, 0) >> 4;
-  const int64_t head_bytes = (int64_t)page * D;
+  const uint32_t head_bytes = (uint32_t)(page * D);
   auto page_of = [&](int t, int sub) { return table[(min(4 * t + sub, last16) << 4) >> a.log_page]; };
   auto block_of = [&](int id, bool& bad) {
     bad = (uint32_t)id >= (uint64_t)a.n_pages;
-    return (int64_t)(bad ? 0 : id) * a.hk + h;
+    return (uint32_t)(bad ? 0 : id) * (uint32_t)a.hk + (uint32_t)h;      // below 2^31 (checked)
   };
 
-  // Staging: piece p = i * 256 + tid is 16 codes: keys' d 16 (p % (D / 16)) .. of
+  // Staging: piece p = i NT + tid is 16 codes: keys' d 16 (p % (D / 16)) .. of
   // key p / (D / 16), and values' positions 16 (p % 4) .. of row d = p / 4.
+  const int sub_v = tid & 3;                             // NT is a multiple of 4
+  const uint8_t* kbase = a.k + (tid % JD) * 16;
+  const uint8_t* vbase = a.v + (tid >> 2) * page;
   uint4 rk[NP], rv[NP];
   float nks = 0.f, nvs = 0.f;                            // the lane's 16 positions' scales, of the block in flight
   int nhave = 0, nkeep = 0;
@@ -875,26 +879,27 @@ __global__ __launch_bounds__(256, RT == 2 ? 2 : 1) void k_kv_prompt(const AttnAr
   int id_k[NP], id_v, id_s;
   auto load_ids = [&](int t) {
 #pragma unroll
-    for (int i = 0; i < NP; ++i) id_k[i] = page_of(t, (i * 256 + tid) / JD >> 4);
-    id_v = page_of(t, tid & 3);
+    for (int i = 0; i < NP; ++i) id_k[i] = page_of(t, (i * NT + tid) / JD >> 4);
+    id_v = page_of(t, sub_v);
     id_s = page_of(t, g);
   };
   auto load = [&](int t) {
     bool bad;
+    const int rest = last16 - 4 * t;                     // 16-position groups behind the block's first
+    const int in_page = 64 * t & (page - 1);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int p = i * 256 + tid, key = p / JD;
-      const int64_t blk = block_of(id_k[i], bad);
-      const int slot = ((min(4 * t + (key >> 4), last16) << 4) & (page - 1)) + (key & 15);
-      rk[i] = *(const uint4*)(a.k + blk * head_bytes + (int64_t)slot * D + (p % JD) * 16);
+      const int key = (i * NT + tid) / JD;
+      const uint32_t blk = block_of(id_k[i], bad);
+      const int slot = ((in_page + (min(key >> 4, rest) << 4)) & (page - 1)) + (key & 15);
+      rk[i] = *(const uint4*)(kbase + (uint64_t)blk * head_bytes + (uint32_t)(slot * D));
     }
-    const int sub = tid & 3;                             // of the thread's values: 256 is a multiple of 4
-    const int64_t blk = block_of(id_v, bad);
-    const uint8_t* vp = a.v + blk * head_bytes + ((min(4 * t + sub, last16) << 4) & (page - 1));
-    nkeep = bad ? 0 : s.len - 64 * t - 16 * sub;
+    const uint32_t blk = block_of(id_v, bad);
+    const uint8_t* vp = vbase + (uint64_t)blk * head_bytes + (uint32_t)((in_page + (min(sub_v, rest) << 4)) & (page - 1));
+    nkeep = bad ? 0 : s.len - 64 * t - 16 * sub_v;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) rv[i] = *(const uint4*)(vp + (i * 64 + (tid >> 2)) * page);
-    const int64_t bg = block_of(id_s, bad);
+    for (int i = 0; i < NP; ++i) rv[i] = *(const uint4*)(vp + i * (NT / 4) * page);
+    const uint32_t bg = block_of(id_s, bad);
     nks = a.ks[bg];
     nvs = a.vs[bg];
     nhave = bad ? 0 : min(max(s.len - 64 * t - 16 * g, 0), 16);
@@ -920,12 +925,12 @@ __global__ __launch_bounds__(256, RT == 2 ? 2 : 1) void k_kv_prompt(const AttnAr
           at |= (((top >> 7) * 0x01020408u) >> 24 & 15u) << (4 * j);
         }
         rv[i] = make_uint4(u[0], u[1], u[2], u[3]);
-        nan_at[buf][i * 64 + (tid >> 2)][tid & 3] = (uint16_t)at;
+        nan_at[buf][i * (NT / 4) + (tid >> 2)][tid & 3] = (uint16_t)at;
       }
     }
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int p = i * 256 + tid, key = p / JD, c = (p % JD) * 2;
+      const int p = i * NT + tid, key = p / JD, c = (p % JD) * 2;
       uint8_t* kr = smem[buf][0] + key * (2 * D);
       *(half8*)(kr + key_chunk<D>(key, c) * 16) = codes8<DT>(rk[i].x, rk[i].y);
       *(half8*)(kr + key_chunk<D>(key, c + 1) * 16) = codes8<DT>(rk[i].z, rk[i].w);
@@ -978,21 +983,18 @@ __global__ __launch_bounds__(256, RT == 2 ? 2 : 1) void k_kv_prompt(const AttnAr
         for (int ks = 0; ks < KS; ++ks) kf[(jt + 1) & 1][ks] = *(const half8*)(kr + koff[ks] + (jt + 1) * 8 * D);
       }
 #pragma unroll
-      for (int i = 0; i < RT; ++i) sc[i][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int i = 0; i < RT; ++i) sc[i][jt] = mfma16(kf[jt & 1][ks], qf[i][ks], sc[i][jt]);
+        for (int i = 0; i < RT; ++i)
+          sc[i][jt] = mfma16(kf[jt & 1][ks], qf[i][ks], ks ? sc[i][jt] : f32x4{0.f, 0.f, 0.f, 0.f});
       __builtin_amdgcn_sched_barrier(0);
     }
     // positive, so that the maximum can be taken before it, and never zero, so
     // that a masked score stays -inf
     const float f = fmaxf(kscale * a.scale_log2, 0x1p-126f);
-    float mx[RT];
-    bool grow = false;
+    if (edge) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      if (edge) {
+      for (int i = 0; i < RT; ++i) {
         const int seen = min(lim[i] - key0, have);       // of the lane's 16 positions
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt)
@@ -1000,22 +1002,50 @@ __global__ __launch_bounds__(256, RT == 2 ? 2 : 1) void k_kv_prompt(const AttnAr
           for (int r = 0; r < 4; ++r)
             if (4 * jt + r >= seen) sc[i][jt][r] = -INFINITY;
       }
-      float y = sc[i][0][0];
-#pragma unroll
-      for (int jt = 0; jt < 4; ++jt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) y = fmaxf(y, sc[i][jt][r]);
-      mx[i] = y * f;                                     // of the lane's positions: enough to ask
-      grow = grow || mx[i] > m[i] + kLazy;
     }
     const float lv = have > 0 ? __builtin_amdgcn_logf(vscale) : -INFINITY;
-    if (__any(grow || lv > vref + kLazyV)) {
+    f16x8 pf[RT][2];
+    float sum[RT], rc;
+    // w = 2^(s f + log2 c - m), c the lane's value scale over the reference; the
+    // softmax's sum takes 1 / c once for the lane's 16 positions
+    auto weights = [&]() {
+      const float lc = have > 0 ? fmaxf(lv - vref, kLowC) : 0.0f;
+      rc = __builtin_amdgcn_exp2f(-lc);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        // a row that has seen nothing yet has m = -inf: its scores are all -inf
+        const float ms = lc - (m[i] == -INFINITY ? 0.0f : m[i]);
+        sum[i] = 0.f;
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i][jt][r], f, ms));
+            sum[i] += w;
+            pf[i][jt >> 1][4 * (jt & 1) + r] = (_Float16)w;
+          }
+      }
+    };
+    // The subtracted maximum and the value reference stay as they are while the
+    // lane's weights sum to at most kMostSum (each is then within fp16): that is
+    // asked after the fact, and only a block that exceeds it has its maximum
+    // taken and its weights formed again.
+    weights();
+    bool grow = lv > vref + kLazyV;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) grow = grow || m[i] == -INFINITY || sum[i] > kMostSum;
+    if (__any(grow)) {
       const float lvm = max_over_g(lv), vn = lvm > vref + kLazyV ? lvm : vref;
       const float fv = vref == vn ? 1.0f : __builtin_amdgcn_exp2f(vref - vn);
       vref = vn;
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        const float mn = fmaxf(m[i], max_over_g(mx[i]));
+        float y = sc[i][0][0];
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y = fmaxf(y, sc[i][jt][r]);
+        const float mn = fmaxf(m[i], max_over_g(y * f));
         const float al = m[i] == mn ? 1.0f : __builtin_amdgcn_exp2f(m[i] - mn);
         l[i] *= al;
         m[i] = mn;
@@ -1024,48 +1054,34 @@ __global__ __launch_bounds__(256, RT == 2 ? 2 : 1) void k_kv_prompt(const AttnAr
 #pragma unroll
           for (int r = 0; r < 4; ++r) o[i][jd][r] *= al * fv;
       }
+      weights();
     }
-    const float lc = have > 0 ? fmaxf(lv - vref, kLowC) : 0.0f;
-    const float rc = __builtin_amdgcn_exp2f(-lc);
-    f16x8 pf[RT][2];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      // a row that has seen nothing yet has m = -inf: its scores are all -inf
-      const float ms = lc - (m[i] == -INFINITY ? 0.0f : m[i]);
-      float sum = 0.f;
-#pragma unroll
-      for (int jt = 0; jt < 4; ++jt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i][jt][r], f, ms));
-          sum += w;
-          pf[i][jt >> 1][4 * (jt & 1) + r] = (_Float16)w;
-        }
-      l[i] += sum * rc;
-    }
+    for (int i = 0; i < RT; ++i) l[i] += sum[i] * rc;
     const uint8_t* vt = smem[buf][1];
     auto vfrag = [&](int jd, int k2) { return *(const f16x8*)(vt + voff[k2] + jd * 2048); };
-    {
-      f16x8 vf[2][2];
-      vf[0][0] = vfrag(0, 0);
-      vf[0][1] = vfrag(0, 1);
+    f16x8 vf[2][2];                                      // likewise, of a d tile
+    vf[0][0] = vfrag(0, 0);
+    vf[0][1] = vfrag(0, 1);
 #pragma unroll
-      for (int jd = 0; jd < JD; ++jd) {
-        if (jd + 1 < JD) {
-          vf[(jd + 1) & 1][0] = vfrag(jd + 1, 0);
-          vf[(jd + 1) & 1][1] = vfrag(jd + 1, 1);
-        }
-#pragma unroll
-        for (int i = 0; i < RT; ++i) o[i][jd] = mfma16(vf[jd & 1][1], pf[i][1], mfma16(vf[jd & 1][0], pf[i][0], o[i][jd]));
-        __builtin_amdgcn_sched_barrier(0);
+    for (int jd = 0; jd < JD; ++jd) {
+      if (jd + 1 < JD) {
+        vf[(jd + 1) & 1][0] = vfrag(jd + 1, 0);
+        vf[(jd + 1) & 1][1] = vfrag(jd + 1, 1);
       }
+#pragma unroll
+      for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) o[i][jd] = mfma16(vf[jd & 1][k2], pf[i][k2], o[i][jd]);
+      __builtin_amdgcn_sched_barrier(0);
     }
     // Values that are not numbers were taken out of the block, since one row may
     // see what is masked for another: a row that sees one gets NaN. Row d = 16 jd
-    // + .. was put by wave jd % 4.
-    const int4 nan = *(const int4*)nan_of[buf];
-    if (__builtin_amdgcn_readfirstlane(nan.x | nan.y | nan.z | nan.w)) {
-      const int put_by[4] = {nan.x, nan.y, nan.z, nan.w};
+    // + .. was put by wave jd % NW.
+    int put_by[NW], nans = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) nans |= put_by[w] = nan_of[buf][w];
+    if (__builtin_amdgcn_readfirstlane(nans)) {
       uint64_t sees[RT];
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
@@ -1074,7 +1090,7 @@ __global__ __launch_bounds__(256, RT == 2 ? 2 : 1) void k_kv_prompt(const AttnAr
       }
 #pragma unroll
       for (int jd = 0; jd < JD; ++jd) {
-        if (!__builtin_amdgcn_readfirstlane(put_by[jd & 3])) continue;
+        if (!__builtin_amdgcn_readfirstlane(put_by[jd % NW])) continue;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const uint64_t at = *(const uint64_t*)nan_at[buf][16 * jd + 4 * g + r];
@@ -1191,7 +1207,7 @@ void launch_append(const AppendArgs& a, int64_t batch, hipStream_t st) {
 }
 
 struct AttnPlan {
-  bool prompt;
+  bool prompt;                     // the prompts' kernel
   int rt, row_blocks, target, items;
   size_t ml_at, bytes;             // workspace: part_o, then part_ml
 };
@@ -1204,7 +1220,7 @@ AttnPlan plan_attn(int64_t batch, int64_t hk, int64_t group, int d, int64_t max_
   p.prompt = rows > 32;
   if (p.prompt) {
     p.rt = 2;
-    p.row_blocks = (int)((rows + 64 * p.rt - 1) / (64 * p.rt));
+    p.row_blocks = (int)((rows + 127) / 128);
     p.target = p.items = 0;
     p.ml_at = p.bytes = 0;
     return p;
@@ -1229,8 +1245,7 @@ void launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
   if (p.prompt) {
     LaunchTimer t("kv_attn", st);
     const dim3 grid((unsigned)((int64_t)p.row_blocks * a.batch * a.hk));
-    if (p.rt == 2) QAT_LAUNCH((k_kv_prompt<DT, D, 2>), grid, dim3(256), 0, st, a);
-    else QAT_LAUNCH((k_kv_prompt<DT, D, 4>), grid, dim3(256), 0, st, a);
+    QAT_LAUNCH((k_kv_prompt<DT, D>), grid, dim3(256), 0, st, a);
     return;
   }
   {
@@ -1258,7 +1273,7 @@ int32_t check_batch(int32_t dtype, int64_t tokens, int64_t batch, int32_t heads,
   if (log2_page(page) < 0) return QAT_ERR_SHAPE;
   if (tokens < 0 || batch < 0 || heads <= 0 || cols <= 0 || n_pages <= 0 || max_new < 0) return QAT_ERR_SHAPE;
   if (tokens > kMaxCount || batch > kMaxGrid || heads > 1024 || cols * page > kMaxCount || n_pages > kMaxCount ||
-      max_new > kMaxCount)
+      max_new > kMaxCount || n_pages * heads >= (int64_t(1) << 31))
     return QAT_ERR_SHAPE;
   return QAT_OK;
 }
