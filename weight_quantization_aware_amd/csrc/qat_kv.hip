@@ -334,15 +334,15 @@ struct AttnArgs {
   int64_t max_new, max_len;
   uint16_t* out;
   int64_t ldo;
-  int target;                      // work items a key head should have in all; 0: one item a sequence
+  int target;                      // workgroups of a key head; 0: one for each sequence
   int max_rows;                    // max_new * group
   int row_blocks;                  // of a sequence and key head (prompts)
-  float* part_o;                   // [item][key head][max_rows][head_dim]
-  float* part_ml;                  // [item][key head][max_rows][2]
+  float* part_o;                   // [part][key head][max_rows][head_dim]
+  float* part_ml;                  // [part][key head][max_rows][2]
 };
 
 constexpr int kTile = 64;          // positions of a block
-constexpr int kMinTiles = 8;       // blocks of a work item at least: two for each of its four waves
+constexpr int kMinTiles = 8;       // blocks of a run at least: two for each of a workgroup's four waves
 constexpr float kLazy = 8.0f;      // how far (log2) a block's maximum may pass the subtracted one
 constexpr float kLazyV = 4.0f;     // the same of value scales over their reference
 constexpr float kMostSum = 32768.0f; // of a lane's 16 weights, each a fp16 number then
@@ -366,9 +366,11 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
   return s;
 }
 
+// Blocks of a sequence; one at least, so that the rows of a sequence without
+// positions are someone's too.
 __device__ __forceinline__ int tiles_of(const AttnArgs& a, int b) {
   const int64_t len = max(min(min((int64_t)a.lens[b], a.max_len), a.cols << a.log_page), (int64_t)0);
-  return (int)((len + kTile - 1) / kTile);
+  return max((int)((len + kTile - 1) / kTile), 1);
 }
 
 __device__ __forceinline__ int wave_sum(int v) {
@@ -377,42 +379,43 @@ __device__ __forceinline__ int wave_sum(int v) {
   return v;
 }
 
-// Blocks of a work item, from the lengths of the whole batch: about `target`
-// items a key head. Every wave computes it for itself.
-__device__ __forceinline__ int chunk_tiles(const AttnArgs& a) {
+// The blocks of all sequences, one sequence after the other, are dealt to the
+// workgroups of a key head in equal runs, whatever the lengths; a run may end one
+// sequence and begin others. Every wave finds its way for itself.
+// Blocks before sequence b (of all with b = batch).
+__device__ __forceinline__ int64_t tiles_before(const AttnArgs& a, int b) {
   const int lane = threadIdx.x & 63;
-  int total = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 64) total += b0 + lane < a.batch ? tiles_of(a, b0 + lane) : 0;
-  total = wave_sum(total);
-  return max((total + a.target - 1) / a.target, kMinTiles);
+  int64_t n = 0;
+  for (int b0 = 0; b0 < b; b0 += 64) n += wave_sum(b0 + lane < b ? tiles_of(a, b0 + lane) : 0);
+  return n;
 }
 
-__device__ __forceinline__ int items_of(const AttnArgs& a, int b, int chunk) {
-  return (tiles_of(a, b) + chunk - 1) / chunk;
+__device__ __forceinline__ int64_t run_length(const AttnArgs& a, int64_t total) {
+  const int64_t n = (total + a.target - 1) / a.target;
+  return n > kMinTiles ? n : kMinTiles;
 }
 
-// Work item -> (sequence, item within it); false past the last one. A sequence
-// without positions has one item all the same: its rows get zeros.
-__device__ __forceinline__ bool find_item(const AttnArgs& a, int item, int chunk, int& b, int& within) {
+// The sequence that block `at` (below the total) is in, and the blocks before it.
+__device__ __forceinline__ int seq_at(const AttnArgs& a, int64_t at, int64_t& before) {
   const int lane = threadIdx.x & 63;
+  before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    int cnt = b0 + lane < a.batch ? max(items_of(a, b0 + lane, chunk), 1) : 0;
+    const int cnt = b0 + lane < a.batch ? tiles_of(a, b0 + lane) : 0;
     int inc = cnt;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int up = __shfl_up(inc, o);
       if (lane >= o) inc += up;
     }
-    const uint64_t past = __ballot(inc > item);
+    const uint64_t past = __ballot(before + inc > at);
     if (past) {
       const int l = __builtin_ctzll(past);
-      b = b0 + l;
-      within = item - __shfl(inc - cnt, l);
-      return true;
+      before += __shfl(inc - cnt, l);
+      return b0 + l;
     }
-    item -= __shfl(inc, 63);
+    before += __shfl(inc, 63);
   }
-  return false;
+  return a.batch - 1;
 }
 
 // Largest value over the four lanes that share lane & 15.
@@ -494,9 +497,10 @@ __device__ __forceinline__ uint4 first_bytes(uint4 u, int n) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int DT, int D, int RT>
+template <int DT, int D>
 __global__ __launch_bounds__(256, 2) void k_kv_decode(const AttnArgs a) {
   typedef typename Half8<DT>::v half8;
+  constexpr int RT = 1;                                  // row tiles of a wave; two spill at head_dim 128
   constexpr int KP = D / 64, JD = D / 16, KS = D / 32;
   constexpr int kPitch = D + 4;
   __shared__ __attribute__((aligned(16))) float so[4][16][kPitch];
@@ -504,280 +508,290 @@ __global__ __launch_bounds__(256, 2) void k_kv_decode(const AttnArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   const int h = blockIdx.y;
-  int b = blockIdx.x, within = 0, chunk = 0;
+  // this workgroup's run of blocks: [at, end), in sequence b behind `before`
+  int b = blockIdx.x;
+  int64_t at_block = 0, end_block = 0, before = 0;
   if (a.target) {
-    chunk = chunk_tiles(a);
-    if (!find_item(a, blockIdx.x, chunk, b, within)) return;
+    const int64_t total = tiles_before(a, a.batch), run = run_length(a, total);
+    at_block = (int64_t)blockIdx.x * run;
+    if (at_block >= total) return;
+    end_block = min(at_block + run, total);
+    b = seq_at(a, at_block, before);
   }
-  b = __builtin_amdgcn_readfirstlane(b);
-  within = __builtin_amdgcn_readfirstlane(within);
-  const Seq s = seq_of(a, b);
-  const int row_base = blockIdx.z * 16 * RT;
-  const int rows = s.n * a.group;
-  if (row_base >= rows) return;
-  const int tiles = (s.len + kTile - 1) / kTile;
-  int t0 = 0, t1 = tiles;
-  bool whole = true;
-  if (a.target) {
-    t0 = within * chunk;
-    t1 = min(t0 + chunk, tiles);
-    whole = tiles <= chunk;
-  }
+  bool first_seq = true;
+  do {
+    b = __builtin_amdgcn_readfirstlane(b);
+    const Seq s = seq_of(a, b);
+    const int row_base = blockIdx.z * 16 * RT;
+    const int rows = s.n * a.group;
+    const int all = max((s.len + kTile - 1) / kTile, 1);   // as tiles_of
+    const int t0 = a.target ? __builtin_amdgcn_readfirstlane((int)(at_block - before)) : 0;
+    const int t_end = a.target ? __builtin_amdgcn_readfirstlane((int)min(end_block - before, (int64_t)all)) : all;
+    const bool whole = t0 == 0 && t_end == all;
+    at_block = before + t_end;
+    before += all;
+    if (row_base < rows) {
+      if (!first_seq) __syncthreads();                       // the last sequence's parts have been read from LDS
+      first_seq = false;
 
-  // this lane's rows, their limits (positions below are seen) and queries
-  half8 qf[RT][KS];
-  int lim[RT], lo_lim = 0x7FFFFFFF, hi_lim = 0;
+      // this lane's rows, their limits (positions below are seen) and queries
+      half8 qf[RT][KS];
+      int lim[RT], lo_lim = 0x7FFFFFFF, hi_lim = 0;
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const int row = row_base + 16 * i + r16;
-    const int rc = min(row, rows - 1);
-    const int tok = rc / a.group, hh = rc - tok * a.group;
-    const int64_t seen = a.causal ? s.start + tok + 1 : (int64_t)s.len;
-    lim[i] = (int)max(min(seen, (int64_t)s.len), (int64_t)0);
-    lo_lim = min(lo_lim, lim[i]);
-    hi_lim = max(hi_lim, lim[i]);
-    const uint16_t* qp = a.q + (s.c0 + tok) * a.ldq + (int64_t)(h * a.group + hh) * D + D / 4 * g;
+      for (int i = 0; i < RT; ++i) {
+        const int row = row_base + 16 * i + r16;
+        const int rc = min(row, rows - 1);
+        const int tok = rc / a.group, hh = rc - tok * a.group;
+        const int64_t seen = a.causal ? s.start + tok + 1 : (int64_t)s.len;
+        lim[i] = (int)max(min(seen, (int64_t)s.len), (int64_t)0);
+        lo_lim = min(lo_lim, lim[i]);
+        hi_lim = max(hi_lim, lim[i]);
+        const uint16_t* qp = a.q + (s.c0 + tok) * a.ldq + (int64_t)(h * a.group + hh) * D + D / 4 * g;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) qf[i][ks] = *(const half8*)(qp + 8 * ks);
-  }
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) {
-    lo_lim = min(lo_lim, __shfl_xor(lo_lim, o));
-    hi_lim = max(hi_lim, __shfl_xor(hi_lim, o));
-  }
-  lo_lim = __builtin_amdgcn_readfirstlane(lo_lim);
-  hi_lim = __builtin_amdgcn_readfirstlane(hi_lim);
-  t1 = min(t1, (hi_lim + kTile - 1) / kTile);
-  const bool one_limit = lo_lim == hi_lim;
-
-  const int32_t* table = a.table + b * a.cols;
-  const int page = 1 << a.log_page;
-  const int last16 = max(s.len - 1, 0) >> 4;             // the last 16 positions that hold any
-  const int64_t head_bytes = (int64_t)page * D;
-
-  // A block's keys and values are in registers once: the next block's keys are
-  // loaded as soon as the scores have been formed, its values as soon as the
-  // output has been, so each load has the other half of a block's work and
-  // the next scores to arrive in.
-  // Page ids of the two 16-position groups a lane loads from: r16 / 4 for
-  // keys, g for values and scales.
-  auto page_of = [&](int t, int sub) { return table[(min(4 * t + sub, last16) << 4) >> a.log_page]; };
-  uint4 xk[4][KP], xv[JD];
-  float xks = 0.f, xvs = 0.f;      // scales of the lane's 16 positions
-  int have = 0;                    // how many of them the cache holds (0: none, or a page left out)
-  int id_a = 0, id_g = 0;          // pages of the block to load next
-  auto load_k = [&](int t) {
-    const int sub = min(4 * t + (r16 >> 2), last16);
-    const int64_t blk = (int64_t)((uint32_t)id_a < (uint64_t)a.n_pages ? id_a : 0) * a.hk + h;
-    const uint8_t* kp = a.k + blk * head_bytes + (int64_t)(((sub << 4) & (page - 1)) + (r16 & 3)) * D + D / 4 * g;
-#pragma unroll
-    for (int jt = 0; jt < 4; ++jt)
-#pragma unroll
-      for (int p = 0; p < KP; ++p) xk[jt][p] = *(const uint4*)(kp + 4 * jt * D + 16 * p);
-  };
-  auto load_v = [&](int t) {
-    const bool bad = (uint32_t)id_g >= (uint64_t)a.n_pages;
-    const int sub = min(4 * t + g, last16);
-    const int64_t blk = (int64_t)(bad ? 0 : id_g) * a.hk + h;
-    const uint8_t* vp = a.v + blk * head_bytes + ((sub << 4) & (page - 1)) + r16 * page;
-#pragma unroll
-    for (int jd = 0; jd < JD; ++jd) xv[jd] = *(const uint4*)(vp + 16 * jd * page);
-    xks = a.ks[blk];
-    xvs = a.vs[blk];
-    have = bad ? 0 : min(max(s.len - 64 * t - 16 * g, 0), 16);
-  };
-
-  f32x4 o[RT][JD];
-  float m[RT], l[RT];                                    // l: this lane's share of the row's sum
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    m[i] = -INFINITY;
-    l[i] = 0.f;
-#pragma unroll
-    for (int jd = 0; jd < JD; ++jd) o[i][jd] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-  float vref = -INFINITY;                                // log2 of the value scales' reference, wave-uniform
-
-  auto compute = [&](int t, bool more) {
-    // some position of the block is masked for some row, absent, or in a page left out
-    const bool edge = 64 * t + 64 > lo_lim || __any(have < 16);
-    f32x4 sc[RT][4];
-#pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-#pragma unroll
-      for (int i = 0; i < RT; ++i) sc[i][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const uint4 u = xk[jt][ks >> 1];
-        const half8 kf = (ks & 1) ? codes8<DT>(u.z, u.w) : codes8<DT>(u.x, u.y);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) sc[i][jt] = mfma16(kf, qf[i][ks], sc[i][jt]);
+        for (int ks = 0; ks < KS; ++ks) qf[i][ks] = *(const half8*)(qp + 8 * ks);
       }
-    }
-    if (more) load_k(t + 4);
-    // positive, so that the maximum can be taken before it, and never zero, so
-    // that a masked score stays -inf
-    const float f = fmaxf(xks * a.scale_log2, 0x1p-126f);
-    const int key0 = 64 * t + 16 * g;
-    float mx[RT];
-    bool grow = false;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      if (edge) {
-        const int seen = min(lim[i] - key0, have);       // of the lane's 16 positions
+      for (int o = 1; o < 16; o <<= 1) {
+        lo_lim = min(lo_lim, __shfl_xor(lo_lim, o));
+        hi_lim = max(hi_lim, __shfl_xor(hi_lim, o));
+      }
+      lo_lim = __builtin_amdgcn_readfirstlane(lo_lim);
+      hi_lim = __builtin_amdgcn_readfirstlane(hi_lim);
+      const int t1 = min(t_end, (hi_lim + kTile - 1) / kTile);
+      const bool one_limit = lo_lim == hi_lim;
+
+      const int32_t* table = a.table + b * a.cols;
+      const int page = 1 << a.log_page;
+      const int last16 = max(s.len - 1, 0) >> 4;             // the last 16 positions that hold any
+      const int64_t head_bytes = (int64_t)page * D;
+
+      // A block's keys and values are in registers once: the next block's keys are
+      // loaded as soon as the scores have been formed, its values as soon as the
+      // output has been, so each load has the other half of a block's work and
+      // the next scores to arrive in.
+      // Page ids of the two 16-position groups a lane loads from: r16 / 4 for
+      // keys, g for values and scales.
+      auto page_of = [&](int t, int sub) { return table[(min(4 * t + sub, last16) << 4) >> a.log_page]; };
+      uint4 xk[4][KP], xv[JD];
+      float xks = 0.f, xvs = 0.f;      // scales of the lane's 16 positions
+      int have = 0;                    // how many of them the cache holds (0: none, or a page left out)
+      int id_a = 0, id_g = 0;          // pages of the block to load next
+      auto load_k = [&](int t) {
+        const int sub = min(4 * t + (r16 >> 2), last16);
+        const int64_t blk = (int64_t)((uint32_t)id_a < (uint64_t)a.n_pages ? id_a : 0) * a.hk + h;
+        const uint8_t* kp = a.k + blk * head_bytes + (int64_t)(((sub << 4) & (page - 1)) + (r16 & 3)) * D + D / 4 * g;
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (4 * jt + r >= seen) sc[i][jt][r] = -INFINITY;
-      }
-      float y = sc[i][0][0];
+          for (int p = 0; p < KP; ++p) xk[jt][p] = *(const uint4*)(kp + 4 * jt * D + 16 * p);
+      };
+      auto load_v = [&](int t) {
+        const bool bad = (uint32_t)id_g >= (uint64_t)a.n_pages;
+        const int sub = min(4 * t + g, last16);
+        const int64_t blk = (int64_t)(bad ? 0 : id_g) * a.hk + h;
+        const uint8_t* vp = a.v + blk * head_bytes + ((sub << 4) & (page - 1)) + r16 * page;
 #pragma unroll
-      for (int jt = 0; jt < 4; ++jt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) y = fmaxf(y, sc[i][jt][r]);
-      mx[i] = y * f;                                     // of the lane's positions: enough to ask
-      grow = grow || mx[i] > m[i] + kLazy;
-    }
-    const float lv = have > 0 ? __builtin_amdgcn_logf(xvs) : -INFINITY;
-    if (__any(grow || lv > vref + kLazyV)) {
-      const float lvm = max_over_g(lv), vn = lvm > vref + kLazyV ? lvm : vref;
-      const float fv = vref == vn ? 1.0f : __builtin_amdgcn_exp2f(vref - vn);
-      vref = vn;
+        for (int jd = 0; jd < JD; ++jd) xv[jd] = *(const uint4*)(vp + 16 * jd * page);
+        xks = a.ks[blk];
+        xvs = a.vs[blk];
+        have = bad ? 0 : min(max(s.len - 64 * t - 16 * g, 0), 16);
+      };
+
+      f32x4 o[RT][JD];
+      float m[RT], l[RT];                                    // l: this lane's share of the row's sum
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        const float mn = fmaxf(m[i], max_over_g(mx[i]));
-        const float al = m[i] == mn ? 1.0f : __builtin_amdgcn_exp2f(m[i] - mn);
-        l[i] *= al;
-        m[i] = mn;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
 #pragma unroll
-        for (int jd = 0; jd < JD; ++jd)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) o[i][jd][r] *= al * fv;
+        for (int jd = 0; jd < JD; ++jd) o[i][jd] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
-    }
-    // w = 2^(s f + log2 c - m), c the lane's value scale over the reference; the
-    // softmax's sum takes 1 / c once for the lane's 16 positions
-    const float lc = have > 0 ? fmaxf(lv - vref, kLowC) : 0.0f;
-    const float rc = __builtin_amdgcn_exp2f(-lc);
-    f16x8 pf[RT][2];
+      float vref = -INFINITY;                                // log2 of the value scales' reference, wave-uniform
+
+      auto compute = [&](int t, bool more) {
+        // some position of the block is masked for some row, absent, or in a page left out
+        const bool edge = 64 * t + 64 > lo_lim || __any(have < 16);
+        f32x4 sc[RT][4];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      // a row that has seen nothing yet has m = -inf: its scores are all -inf
-      const float ms = lc - (m[i] == -INFINITY ? 0.0f : m[i]);
-      float sum = 0.f;
+        for (int jt = 0; jt < 4; ++jt) {
 #pragma unroll
-      for (int jt = 0; jt < 4; ++jt)
+          for (int i = 0; i < RT; ++i) sc[i][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i][jt][r], f, ms));
-          sum += w;
-          pf[i][jt >> 1][4 * (jt & 1) + r] = (_Float16)w;
-        }
-      l[i] += sum * rc;
-    }
-    if (!edge) {
+          for (int ks = 0; ks < KS; ++ks) {
+            const uint4 u = xk[jt][ks >> 1];
+            const half8 kf = (ks & 1) ? codes8<DT>(u.z, u.w) : codes8<DT>(u.x, u.y);
 #pragma unroll
-      for (int jd = 0; jd < JD; ++jd) {
-        const f16x8 v0 = codes8<QAT_F16>(xv[jd].x, xv[jd].y), v1 = codes8<QAT_F16>(xv[jd].z, xv[jd].w);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) o[i][jd] = mfma16(v1, pf[i][1], mfma16(v0, pf[i][0], o[i][jd]));
-      }
-    } else {
-      // Absent positions' values are zeroed whatever they hold. Where the rows'
-      // limits differ, a value that is not a number may be seen by one row and
-      // masked for another: it is taken out of the product, and counted apart
-      // against the positions that each row sees.
-      const int keep = one_limit ? min(lo_lim - key0, have) : have;
-#pragma unroll
-      for (int jd = 0; jd < JD; ++jd) {
-        const uint4 u = first_bytes(xv[jd], keep);
-        f16x8 v0 = codes8<QAT_F16>(u.x, u.y), v1 = codes8<QAT_F16>(u.z, u.w);
-        if (!one_limit) {
-          const f16x8 n0 = take_nan(v0), n1 = take_nan(v1);
-#pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            const int seen = min(lim[i] - key0, have);
-            const f32x4 cnt = mfma16(n1, ones8(seen - 8), mfma16(n0, ones8(seen), f32x4{0.f, 0.f, 0.f, 0.f}));
-#pragma unroll
-            for (int r = 0; r < 4; ++r) o[i][jd][r] = cnt[r] > 0.f ? NAN : o[i][jd][r];
+            for (int i = 0; i < RT; ++i) sc[i][jt] = mfma16(kf, qf[i][ks], sc[i][jt]);
           }
         }
+        if (more) load_k(t + 4);
+        // positive, so that the maximum can be taken before it, and never zero, so
+        // that a masked score stays -inf
+        const float f = fmaxf(xks * a.scale_log2, 0x1p-126f);
+        const int key0 = 64 * t + 16 * g;
+        float mx[RT];
+        bool grow = false;
 #pragma unroll
-        for (int i = 0; i < RT; ++i) o[i][jd] = mfma16(v1, pf[i][1], mfma16(v0, pf[i][0], o[i][jd]));
+        for (int i = 0; i < RT; ++i) {
+          if (edge) {
+            const int seen = min(lim[i] - key0, have);       // of the lane's 16 positions
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (4 * jt + r >= seen) sc[i][jt][r] = -INFINITY;
+          }
+          float y = sc[i][0][0];
+#pragma unroll
+          for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y = fmaxf(y, sc[i][jt][r]);
+          mx[i] = y * f;                                     // of the lane's positions: enough to ask
+          grow = grow || mx[i] > m[i] + kLazy;
+        }
+        const float lv = have > 0 ? __builtin_amdgcn_logf(xvs) : -INFINITY;
+        if (__any(grow || lv > vref + kLazyV)) {
+          const float lvm = max_over_g(lv), vn = lvm > vref + kLazyV ? lvm : vref;
+          const float fv = vref == vn ? 1.0f : __builtin_amdgcn_exp2f(vref - vn);
+          vref = vn;
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            const float mn = fmaxf(m[i], max_over_g(mx[i]));
+            const float al = m[i] == mn ? 1.0f : __builtin_amdgcn_exp2f(m[i] - mn);
+            l[i] *= al;
+            m[i] = mn;
+#pragma unroll
+            for (int jd = 0; jd < JD; ++jd)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) o[i][jd][r] *= al * fv;
+          }
+        }
+        // w = 2^(s f + log2 c - m), c the lane's value scale over the reference; the
+        // softmax's sum takes 1 / c once for the lane's 16 positions
+        const float lc = have > 0 ? fmaxf(lv - vref, kLowC) : 0.0f;
+        const float rc = __builtin_amdgcn_exp2f(-lc);
+        f16x8 pf[RT][2];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          // a row that has seen nothing yet has m = -inf: its scores are all -inf
+          const float ms = lc - (m[i] == -INFINITY ? 0.0f : m[i]);
+          float sum = 0.f;
+#pragma unroll
+          for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i][jt][r], f, ms));
+              sum += w;
+              pf[i][jt >> 1][4 * (jt & 1) + r] = (_Float16)w;
+            }
+          l[i] += sum * rc;
+        }
+        if (!edge) {
+#pragma unroll
+          for (int jd = 0; jd < JD; ++jd) {
+            const f16x8 v0 = codes8<QAT_F16>(xv[jd].x, xv[jd].y), v1 = codes8<QAT_F16>(xv[jd].z, xv[jd].w);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) o[i][jd] = mfma16(v1, pf[i][1], mfma16(v0, pf[i][0], o[i][jd]));
+          }
+        } else {
+          // Absent positions' values are zeroed whatever they hold. Where the rows'
+          // limits differ, a value that is not a number may be seen by one row and
+          // masked for another: it is taken out of the product, and counted apart
+          // against the positions that each row sees.
+          const int keep = one_limit ? min(lo_lim - key0, have) : have;
+#pragma unroll
+          for (int jd = 0; jd < JD; ++jd) {
+            const uint4 u = first_bytes(xv[jd], keep);
+            f16x8 v0 = codes8<QAT_F16>(u.x, u.y), v1 = codes8<QAT_F16>(u.z, u.w);
+            if (!one_limit) {
+              const f16x8 n0 = take_nan(v0), n1 = take_nan(v1);
+#pragma unroll
+              for (int i = 0; i < RT; ++i) {
+                const int seen = min(lim[i] - key0, have);
+                const f32x4 cnt = mfma16(n1, ones8(seen - 8), mfma16(n0, ones8(seen), f32x4{0.f, 0.f, 0.f, 0.f}));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[i][jd][r] = cnt[r] > 0.f ? NAN : o[i][jd][r];
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < RT; ++i) o[i][jd] = mfma16(v1, pf[i][1], mfma16(v0, pf[i][0], o[i][jd]));
+          }
+        }
+        if (more) {
+          load_v(t + 4);
+          if (t + 8 < t1) {
+            id_a = page_of(t + 8, r16 >> 2);
+            id_g = page_of(t + 8, g);
+          }
+        }
+      };
+
+      int t = t0 + wave;
+      if (t < t1) {
+        id_a = page_of(t, r16 >> 2);
+        id_g = page_of(t, g);
+        load_k(t);
+        load_v(t);
+        if (t + 4 < t1) {
+          id_a = page_of(t + 4, r16 >> 2);
+          id_g = page_of(t + 4, g);
+        }
+        for (; t < t1; t += 4) compute(t, t + 4 < t1);
+      }
+
+      // the four waves meet in LDS, 16 rows at a time
+      const float vscale = vref == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(vref);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        if (i) __syncthreads();
+#pragma unroll
+        for (int jd = 0; jd < JD; ++jd) {
+          const f32x4 v = o[i][jd];
+          *(f32x4*)&so[wave][r16][16 * jd + 4 * g] = f32x4{v[0] * vscale, v[1] * vscale, v[2] * vscale, v[3] * vscale};
+        }
+        float row_sum = l[i];
+        row_sum += __shfl_xor(row_sum, 16);
+        row_sum += __shfl_xor(row_sum, 32);
+        if (g == 0) {
+          sm[wave][r16] = m[i];
+          sl[wave][r16] = row_sum;
+        }
+        __syncthreads();
+        const int rr = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * (D / 16);
+        const int row = row_base + 16 * i + rr;
+        if (row >= rows) continue;
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) mm = fmaxf(mm, sm[w][rr]);
+        float ll = 0.f, acc[D / 16];
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) acc[j] = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          if (sl[w][rr] == 0.f) continue;                    // saw nothing
+          const float f = __builtin_amdgcn_exp2f(sm[w][rr] - mm);
+          ll += sl[w][rr] * f;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) acc[j] += so[w][rr][d0 + j] * f;
+        }
+        if (whole) {
+          const float inv = ll == 0.f ? 0.0f : 1.0f / ll;
+          const int tok = row / a.group, hh = row - tok * a.group;
+          uint16_t* op = a.out + (s.c0 + tok) * a.ldo + (int64_t)(h * a.group + hh) * D + d0;
+#pragma unroll
+          for (int j = 0; j < D / 16; j += 2) *(uint32_t*)(op + j) = pack2<DT>(acc[j] * inv, acc[j + 1] * inv);
+        } else {
+          // part (workgroup + sequence): along the runs one of the two grows from part to part
+          const int64_t at = ((int64_t)((int)blockIdx.x + b) * a.hk + h) * a.max_rows + row;
+#pragma unroll
+          for (int j = 0; j < D / 16; j += 4)
+            *(f32x4*)(a.part_o + at * D + d0 + j) = f32x4{acc[j], acc[j + 1], acc[j + 2], acc[j + 3]};
+          if (d0 == 0) *(f32x2*)(a.part_ml + at * 2) = f32x2{mm, ll};
+        }
       }
     }
-    if (more) {
-      load_v(t + 4);
-      if (t + 8 < t1) {
-        id_a = page_of(t + 8, r16 >> 2);
-        id_g = page_of(t + 8, g);
-      }
-    }
-  };
-
-  int t = t0 + wave;
-  if (t < t1) {
-    id_a = page_of(t, r16 >> 2);
-    id_g = page_of(t, g);
-    load_k(t);
-    load_v(t);
-    if (t + 4 < t1) {
-      id_a = page_of(t + 4, r16 >> 2);
-      id_g = page_of(t + 4, g);
-    }
-    for (; t < t1; t += 4) compute(t, t + 4 < t1);
-  }
-
-  // the four waves meet in LDS, 16 rows at a time
-  const float vscale = vref == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(vref);
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    if (i) __syncthreads();
-#pragma unroll
-    for (int jd = 0; jd < JD; ++jd) {
-      const f32x4 v = o[i][jd];
-      *(f32x4*)&so[wave][r16][16 * jd + 4 * g] = f32x4{v[0] * vscale, v[1] * vscale, v[2] * vscale, v[3] * vscale};
-    }
-    float row_sum = l[i];
-    row_sum += __shfl_xor(row_sum, 16);
-    row_sum += __shfl_xor(row_sum, 32);
-    if (g == 0) {
-      sm[wave][r16] = m[i];
-      sl[wave][r16] = row_sum;
-    }
-    __syncthreads();
-    const int rr = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * (D / 16);
-    const int row = row_base + 16 * i + rr;
-    if (row >= rows) continue;
-    float mm = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, sm[w][rr]);
-    float ll = 0.f, acc[D / 16];
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) acc[j] = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if (sl[w][rr] == 0.f) continue;                    // saw nothing
-      const float f = __builtin_amdgcn_exp2f(sm[w][rr] - mm);
-      ll += sl[w][rr] * f;
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) acc[j] += so[w][rr][d0 + j] * f;
-    }
-    if (whole) {
-      const float inv = ll == 0.f ? 0.0f : 1.0f / ll;
-      const int tok = row / a.group, hh = row - tok * a.group;
-      uint16_t* op = a.out + (s.c0 + tok) * a.ldo + (int64_t)(h * a.group + hh) * D + d0;
-#pragma unroll
-      for (int j = 0; j < D / 16; j += 2) *(uint32_t*)(op + j) = pack2<DT>(acc[j] * inv, acc[j + 1] * inv);
-    } else {
-      const int64_t at = ((int64_t)blockIdx.x * a.hk + h) * a.max_rows + row;
-#pragma unroll
-      for (int j = 0; j < D / 16; j += 4)
-        *(f32x4*)(a.part_o + at * D + d0 + j) = f32x4{acc[j], acc[j + 1], acc[j + 2], acc[j + 3]};
-      if (d0 == 0) *(f32x2*)(a.part_ml + at * 2) = f32x2{mm, ll};
-    }
-  }
+    ++b;
+  } while (a.target && at_block < end_block);
 }
 
 // ---------------------------------------------------------------------------
@@ -1150,37 +1164,40 @@ __global__ __launch_bounds__(256, 2) void k_kv_prompt(const AttnArgs a) {
   }
 }
 
-// Joins the items of a split sequence: a wave for each (row, head). Items past
-// a row's limit have stored m = -inf, l = 0.
+// Joins the parts of a split sequence: a wave for each (row, head). Parts past a
+// row's limit have m = -inf, l = 0.
 template <int DT, int D>
 __global__ __launch_bounds__(256) void k_kv_join(const AttnArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int b = blockIdx.x, h = blockIdx.y;
-  const int chunk = chunk_tiles(a);
-  const int items = items_of(a, b, chunk);
-  if (items <= 1) return;
-  int first = 0;
-  for (int b0 = 0; b0 < b; b0 += 64) {
-    first += wave_sum(b0 + lane < b ? max(items_of(a, b0 + lane, chunk), 1) : 0);
-  }
+  const int64_t run = run_length(a, tiles_before(a, a.batch)), before = tiles_before(a, b);
+  const int first = (int)(before / run), parts = (int)((before + tiles_of(a, b) - 1) / run) - first + 1;
+  if (parts <= 1) return;
   const Seq s = seq_of(a, b);
   const int rows = s.n * a.group;
   for (int row = blockIdx.z * 4 + wave; row < rows; row += gridDim.z * 4) {
-    float mm = -INFINITY, ll = 0.f;
+    const int64_t at0 = ((int64_t)(first + b) * a.hk + h) * a.max_rows + row, step = (int64_t)a.hk * a.max_rows;
+    float mm = -INFINITY;
+    for (int i = lane; i < parts; i += 64) {
+      const f32x2 ml = *(const f32x2*)(a.part_ml + (at0 + i * step) * 2);
+      if (ml[1] != 0.f) mm = fmaxf(mm, ml[0]);
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) mm = fmaxf(mm, __shfl_xor(mm, o));
+    float ll = 0.f;
     f32x2 acc{0.f, 0.f};
-    for (int i = 0; i < items; ++i) {
-      const int64_t at = ((int64_t)(first + i) * a.hk + h) * a.max_rows + row;
+#pragma unroll 8
+    for (int i = 0; i < parts; ++i) {
+      const int64_t at = at0 + i * step;
       const f32x2 ml = *(const f32x2*)(a.part_ml + at * 2);
-      if (ml[1] == 0.f) continue;
-      const float mn = fmaxf(mm, ml[0]);
-      const float f0 = mm == mn ? 1.0f : __builtin_amdgcn_exp2f(mm - mn), f1 = __builtin_amdgcn_exp2f(ml[0] - mn);
-      mm = mn;
-      ll = ll * f0 + ml[1] * f1;
       f32x2 v{0.f, 0.f};
       if constexpr (D == 128) v = *(const f32x2*)(a.part_o + at * D + 2 * lane);
       else v[0] = a.part_o[at * D + lane];
-      acc[0] = acc[0] * f0 + v[0] * f1;
-      acc[1] = acc[1] * f0 + v[1] * f1;
+      const bool some = ml[1] != 0.f;                    // NaN counts
+      const float f = some ? __builtin_amdgcn_exp2f(ml[0] - mm) : 0.f;
+      ll += some ? ml[1] * f : 0.f;
+      acc[0] += some ? v[0] * f : 0.f;
+      acc[1] += some ? v[1] * f : 0.f;
     }
     const float inv = ll == 0.f ? 0.0f : 1.0f / ll;
     const int tok = row / a.group, hh = row - tok * a.group;
@@ -1208,32 +1225,30 @@ void launch_append(const AppendArgs& a, int64_t batch, hipStream_t st) {
 
 struct AttnPlan {
   bool prompt;                     // the prompts' kernel
-  int rt, row_blocks, target, items;
+  int row_blocks, target, parts;
   size_t ml_at, bytes;             // workspace: part_o, then part_ml
 };
 
-constexpr int kTargetGroups = 512; // two workgroups on each of 256 CUs
+constexpr int kTargetGroups = 256; // one workgroup for each CU: two measured the same on long caches, slower on short ones
 
 AttnPlan plan_attn(int64_t batch, int64_t hk, int64_t group, int d, int64_t max_new, int64_t max_len) {
   AttnPlan p;
   const int64_t rows = max_new * group;
   p.prompt = rows > 32;
   if (p.prompt) {
-    p.rt = 2;
     p.row_blocks = (int)((rows + 127) / 128);
-    p.target = p.items = 0;
+    p.target = p.parts = 0;
     p.ml_at = p.bytes = 0;
     return p;
   }
-  p.rt = rows <= 16 ? 1 : 2;
-  p.row_blocks = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
+  p.row_blocks = (int)((rows + 15) / 16);
   const int64_t per = hk * p.row_blocks;
   const bool split = max_len > kMinTiles * kTile && per < kTargetGroups;
   p.target = split ? (int)((kTargetGroups + per - 1) / per) : 0;
-  p.items = (int)(batch + p.target);
+  p.parts = (int)(batch + p.target);         // at most
   p.ml_at = p.bytes = 0;
   if (split) {
-    const int64_t n = (int64_t)p.items * hk * rows;
+    const int64_t n = (int64_t)p.parts * hk * rows;
     p.ml_at = (size_t)((n * d * 4 + 255) / 256 * 256);
     p.bytes = p.ml_at + (size_t)((n * 8 + 255) / 256 * 256);
   }
@@ -1250,9 +1265,8 @@ void launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
   }
   {
     LaunchTimer t("kv_attn", st);
-    const dim3 grid((unsigned)(a.target ? p.items : a.batch), (unsigned)a.hk, (unsigned)p.row_blocks);
-    if (p.rt == 1) QAT_LAUNCH((k_kv_decode<DT, D, 1>), grid, dim3(256), 0, st, a);
-    else QAT_LAUNCH((k_kv_decode<DT, D, 2>), grid, dim3(256), 0, st, a);
+    const dim3 grid((unsigned)(a.target ? a.target : a.batch), (unsigned)a.hk, (unsigned)p.row_blocks);
+    QAT_LAUNCH((k_kv_decode<DT, D>), grid, dim3(256), 0, st, a);
   }
   if (a.target) {
     LaunchTimer t("kv_attn_join", st);
