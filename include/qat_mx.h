@@ -49,8 +49,9 @@ enum { QAT_F32 = 0, QAT_BF16 = 1, QAT_F16 = 2 };
 int32_t qat_mx_quant(const void* X, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes,
                      uint8_t* scales, void* X_hat, hipStream_t stream);
 
-/* Workspace bytes of qat_mx_gemm and qat_mx_linear at these sizes; 0 for
- * invalid sizes. */
+/* Workspace bytes that serve both qat_mx_gemm and qat_mx_linear at these sizes;
+ * 0 where neither needs one (a few tokens) and for invalid sizes. ws may be NULL
+ * then. */
 size_t qat_mx_ws_bytes(int64_t M, int64_t out, int64_t in);
 
 /*

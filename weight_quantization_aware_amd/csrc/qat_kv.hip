@@ -1220,6 +1220,7 @@ void launch_append(const AppendArgs& a, int64_t batch, hipStream_t st) {
   // flight, no barriers; 256 threads otherwise
   if (most * a.d / 8 <= 64) QAT_LAUNCH((k_kv_append<DT, 64, 1>), grid, dim3(64), lds, st, a);
   else if (most * a.d / 8 <= 512) QAT_LAUNCH((k_kv_append<DT, 256, 2>), grid, dim3(256), lds, st, a);
+  else if (most * a.d / 8 <= 1024) QAT_LAUNCH((k_kv_append<DT, 256, 4>), grid, dim3(256), lds, st, a);
   else QAT_LAUNCH((k_kv_append<DT, 256, 8>), grid, dim3(256), lds, st, a);
 }
 

@@ -157,6 +157,8 @@ struct ProductArgs {
   int M, N, K;
   void* Y;
   int64_t ldy;
+  const void* x16;                 // X in 16 bits, quantised by the product itself
+  int64_t ldx;
 };
 
 // Superstep ss of a row: blocks 16 ss + 4 g .. + 3, those past the row's end zero.
@@ -218,10 +220,21 @@ __device__ __forceinline__ void store_out8(void* Y, int64_t ldy, int m, int n, i
 }
 
 // Few tokens: a workgroup owns 16 weight rows and 16 tokens; its 8 waves split
-// the contraction by supersteps and meet in LDS.
-template <int DT>
+// the contraction by supersteps and meet in LDS. Bound by the weights' bytes and,
+// at these sizes, by latency.
+//
+// kQuant: X comes in 16 bits and is quantised here, one launch for the linear
+// layer of a served token. A wave quantises its own supersteps (8 elements a
+// lane, a token at a time) while its weights arrive, and turns them into the
+// operand's order through its own LDS. Every workgroup does so again, which pays
+// for up to kQuantTokens tokens.
+constexpr int kQuantTokens = 4;
+
+template <int DT, bool kQuant>
 __global__ __launch_bounds__(512) void k_mx_skinny(const ProductArgs a) {
   __shared__ f32x4 part[8][64];
+  // codes and scales of a superstep
+  __shared__ __attribute__((aligned(16))) uint8_t xq[kQuant ? 8 : 1][kQuant ? kQuantTokens : 1][272];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r16 = lane & 15, g = lane >> 4;
   const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
@@ -229,13 +242,29 @@ __global__ __launch_bounds__(512) void k_mx_skinny(const ProductArgs a) {
   const int64_t wr = min(n0 + r16, a.N - 1), xr = min(m0 + r16, a.M - 1);
   const uint8_t* wc = a.wc + wr * (a.K / 2);
   const uint8_t* ws = a.ws + wr * nblk;
-  const uint8_t* xc = a.xc + xr * (a.K / 2);
-  const uint8_t* xs = a.xs + xr * nblk;
   f32x4 acc{0.f, 0.f, 0.f, 0.f};
   for (int ss = wave; ss < nss; ss += 8) {
     Piece w, x;
     load_piece(w, wc, ws, nblk, ss, g);
-    load_piece(x, xc, xs, nblk, ss, g);
+    if constexpr (kQuant) {
+      const int col = ss * 512 + 8 * lane;
+      for (int m = 0; m < a.M; ++m) {
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (col < a.K) load8<DT>(a.x16, m * a.ldx + col, v);       // the same for a block's four lanes
+        uint32_t byte;
+        *(uint32_t*)&xq[wave][m][4 * lane] = quant8(v, byte);
+        if ((lane & 3) == 0) xq[wave][m][256 + (lane >> 2)] = (uint8_t)byte;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x.c[j] = *(const i32x4*)&xq[wave][xr][64 * g + 16 * j];
+      x.s = *(const uint32_t*)&xq[wave][xr][256 + 4 * g];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    } else {
+      load_piece(x, a.xc + xr * (a.K / 2), a.xs + xr * nblk, nblk, ss, g);
+    }
     acc = mfma4(w, x, acc);
   }
   part[wave][lane] = acc;
@@ -717,6 +746,7 @@ struct MxWs {
     auto up = [](int64_t v) { return (size_t)((v + 255) / 256 * 256); };
     const int64_t row = (in + 511) / 512 * 16;
     const bool tile = tiled(M, out, in);
+    if (M <= kQuantTokens) linear = false;                // X is quantised in the product
     MxWs w;
     w.xs = linear ? up(M * in / 2) : 0;
     w.ws = w.xs + (tile ? up(M * row) : linear ? up(M * in / 32) : 0);
@@ -747,8 +777,13 @@ void launch_product(const ProductArgs& a, int dtype, hipStream_t st) {
     return;
   }
   const dim3 grid((a.N + 15) / 16, (a.M + 15) / 16);
-  if (dtype == QAT_BF16) QAT_LAUNCH(k_mx_skinny<QAT_BF16>, grid, dim3(512), 0, st, a);
-  else QAT_LAUNCH(k_mx_skinny<QAT_F16>, grid, dim3(512), 0, st, a);
+  if (a.x16) {
+    if (dtype == QAT_BF16) QAT_LAUNCH((k_mx_skinny<QAT_BF16, true>), grid, dim3(512), 0, st, a);
+    else QAT_LAUNCH((k_mx_skinny<QAT_F16, true>), grid, dim3(512), 0, st, a);
+  } else {
+    if (dtype == QAT_BF16) QAT_LAUNCH((k_mx_skinny<QAT_BF16, false>), grid, dim3(512), 0, st, a);
+    else QAT_LAUNCH((k_mx_skinny<QAT_F16, false>), grid, dim3(512), 0, st, a);
+  }
 }
 
 void launch_gemm(ProductArgs a, int dtype, uint8_t* ws, const MxWs& w, hipStream_t st) {
@@ -765,6 +800,12 @@ void launch_gemm(ProductArgs a, int dtype, uint8_t* ws, const MxWs& w, hipStream
 }
 
 void launch_linear(const void* X, int64_t ldx, ProductArgs a, int dtype, uint8_t* ws, const MxWs& w, hipStream_t st) {
+  if (a.M <= kQuantTokens) {
+    a.x16 = X;
+    a.ldx = ldx;
+    launch_product(a, dtype, st);
+    return;
+  }
   a.xc = ws;
   a.xs = ws + w.xs;
   if (tiled(a.M, a.N, a.K)) {
@@ -839,7 +880,7 @@ QAT_API int32_t qat_mx_gemm(const uint8_t* X_codes, const uint8_t* X_scales, con
   QAT_CHECK(check_spans({{Y, strided_bytes(M, ldy, out, 2)}, {ws, w.bytes}},
                         {{X_codes, (size_t)(M * in / 2)}, {X_scales, (size_t)(M * in / 32)},
                          {W_codes, (size_t)(out * in / 2)}, {W_scales, (size_t)(out * in / 32)}}));
-  ProductArgs a{X_codes, X_scales, W_codes, W_scales, (int)M, (int)out, (int)in, Y, ldy};
+  ProductArgs a{X_codes, X_scales, W_codes, W_scales, (int)M, (int)out, (int)in, Y, ldy, nullptr, 0};
   launch_gemm(a, dtype, (uint8_t*)ws, w, stream);
   return finish_call();
 }
@@ -855,11 +896,11 @@ QAT_API int32_t qat_mx_linear(const void* X, int64_t ldx, const uint8_t* W_codes
   if (ldx % 8 != 0) return QAT_ERR_ALIGN;
   QAT_CHECK(check_aligned({X, W_codes, W_scales, Y, ws}));
   const MxWs w = MxWs::of(M, out, in, true);
-  if (!ws || ws_bytes < w.bytes) return QAT_ERR_WORKSPACE;
+  if (w.bytes && (!ws || ws_bytes < w.bytes)) return QAT_ERR_WORKSPACE;
   QAT_CHECK(check_spans({{Y, strided_bytes(M, ldy, out, 2)}, {ws, w.bytes}},
                         {{X, strided_bytes(M, ldx, in, 2)}, {W_codes, (size_t)(out * in / 2)},
                          {W_scales, (size_t)(out * in / 32)}}));
-  ProductArgs a{nullptr, nullptr, W_codes, W_scales, (int)M, (int)out, (int)in, Y, ldy};
+  ProductArgs a{nullptr, nullptr, W_codes, W_scales, (int)M, (int)out, (int)in, Y, ldy, nullptr, 0};
   launch_linear(X, ldx, a, dtype, (uint8_t*)ws, w, stream);
   return finish_call();
 }
