@@ -469,9 +469,9 @@ class _RowArgs(_Args):
         if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape:
             super().t(name, t, dtypes, shape)                # says what is wrong
         self.seen.append((name, t))
-        row = math.prod(shape[1:])
         if t.is_contiguous():
-            return t.data_ptr(), max(row, 1)
+            return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(math.prod(shape[1:]), 1)
+        row = math.prod(shape[1:])
         want = 1
         for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
             if size != 1 and stride != want:
@@ -487,7 +487,7 @@ class _RowArgs(_Args):
         for _, t in self.seen:
             if t.get_device() != dev or dev < 0:
                 self.done()                                  # says what is wrong
-        if dev == torch.cuda.current_device():
+        if dev == _current_device():
             _call(self.fn, *args, _raw_stream(dev))
         else:
             with torch.cuda.device(dev):
@@ -495,9 +495,13 @@ class _RowArgs(_Args):
 
 
 def _raw_stream(dev: int) -> int:
-    """The current stream's handle on a device, without a Stream object where torch offers that."""
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(dev) if get else torch.cuda.current_stream(dev).cuda_stream
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# The current stream's handle and the current device, without a Stream object
+# and further checks, where torch offers them (a tensor on the GPU is at hand).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _dims(fn: str, name: str, t, n: int, what: str):
