@@ -296,6 +296,11 @@ ATTN = [
     ([128, 64], [192, 64], 3, 3, 128, 128),
     ([70, 33], [600, 33], 10, 5, 64, 64),
     ([200], [1000], 8, 8, 128, 64),
+    # enough workgroups of 128 rows for the prompts' kernel: ragged, empty and short sequences in one batch
+    ([40, 33, 64], [40, 100, 64], 64, 64, 64, 16),
+    ([70, 0, 130, 1], [70, 0, 300, 50], 96, 48, 128, 64),
+    ([129, 5], [191, 500], 80, 80, 128, 128),
+    ([35, 128, 2], [90, 128, 1], 320, 64, 64, 32),
 ]
 
 
@@ -328,23 +333,24 @@ def test_attn_many_sequences():
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_attn_large_scores_and_spread_scales(dtype):
     # probabilities that reach one key only, and value scales 2^12 apart
-    c = Cache([700, 90], 2, 64, 32).fill()
-    for p in range(c.vs.shape[0]):
-        c.vs[p] *= 2.0 ** (p % 13)
-    check_attn(c, rand((2, 4, 64), 1, dtype) * 8, [0, 1, 2], [700, 90], 1.0, True)
+    for hk, cu in ((2, [0, 1, 2]), (96, [0, 40, 80])):
+        c = Cache([700, 90], hk, 64, 32).fill()
+        for p in range(c.vs.shape[0]):
+            c.vs[p] *= 2.0 ** (p % 13)
+        check_attn(c, rand((cu[-1], max(hk, 4), 64), 1, dtype) * 8, cu, [700, 90], 1.0, True)
 
 
-@pytest.mark.parametrize("new", [1, 5, 90])
-def test_attn_masked_nan_stays_out(new):
+@pytest.mark.parametrize("new,hk", [(1, 1), (5, 1), (90, 1), (90, 96)])
+def test_attn_masked_nan_stays_out(new, hk):
     # a key and a value that are not numbers, in the middle of the new tokens: rows before them see
     # neither, rows from them on see both; pages left out and slots behind the end are poison too
     n, d = 200, 64
     for what in ("k", "v"):
-        c = Cache([n], 1, d, 16).fill()
+        c = Cache([n], hk, d, 16).fill()
         at = n - 1 - new // 2
-        getattr(c, what)[c.table[0, at // 16], 0, at % 16, 7] = 0x7F
-        q = rand((new, 2, d), 3, BF)
-        dev, out = c.device(), torch.empty(new, 2, d, dtype=BF, device="cuda")
+        getattr(c, what)[c.table[0, at // 16], :, at % 16, 7] = 0x7F
+        q = rand((new, 2 * hk, d), 3, BF)
+        dev, out = c.device(), torch.empty(new, 2 * hk, d, dtype=BF, device="cuda")
         Q.qat_kv_attn(q, i32([0, new]), i32([n]), c.tab(), *dev, out, 0.125, ws=Q.workspace(1 << 24))
         first = at - (n - new)                  # the first row that sees position `at`
         o = host(out)
@@ -359,6 +365,13 @@ def test_attn_bad_pages_are_left_out():
         c.table[0, 1], c.table[0, -1], c.table[1, 0] = -1, 10 ** 7, c.k.shape[0]
         check_attn(c, rand((4, 4, 64), 1, HF), [0, 3, 4], [300, 130], 0.125, True)
         check_attn(c, rand((4, 4, 64), 1, HF), [0, 3, 4], [300, 130], 0.125, False)
+    big = Cache([300, 130], 96, 64, 32).fill()  # the prompts' kernel
+    big.table[0, 1], big.table[0, -1], big.table[1, 0] = -1, 10 ** 7, big.k.shape[0]
+    check_attn(big, rand((75, 96, 64), 1, HF), [0, 40, 75], [300, 130], 0.125, True)
+    check_attn(big, rand((75, 96, 64), 1, HF), [0, 40, 75], [300, 130], 0.125, False)
+    big.table[:] = -1
+    _, o, _ = check_attn(big, rand((75, 96, 64), 1, HF), [0, 40, 75], [300, 130], 0.125, True)
+    assert (o == 0).all()
     c.table[:] = -1                             # nothing is left
     _, o, _ = check_attn(c, rand((4, 4, 64), 1, HF), [0, 3, 4], [300, 130], 0.125, True)
     assert (o == 0).all()
@@ -413,9 +426,10 @@ def test_attn_of_a_cache_past_32_bit_offsets():
     assert torch.equal(outs[0], outs[1]) and torch.isfinite(outs[0].float()).all()
 
 
-@pytest.mark.parametrize("new,lens", [([1, 1, 1], [1500, 900, 40]), ([100, 20, 3], [100, 300, 3])])
-def test_attn_replayed_graphs_share_a_workspace(new, lens):
-    hq, hk, d = 8, 2, 64
+@pytest.mark.parametrize("new,lens,hk", [([1, 1, 1], [1500, 900, 40], 2), ([100, 20, 3], [100, 300, 3], 2),
+                                         ([100, 20, 3], [100, 300, 3], 32)])
+def test_attn_replayed_graphs_share_a_workspace(new, lens, hk):
+    hq, d = 4 * hk, 64
     c = Cache([l + 8 for l in lens], hk, d, 32).fill()
     dev, tab, cu = c.device(), c.tab(), i32(np.concatenate([[0], np.cumsum(new)]).tolist())
     ln = i32(lens)

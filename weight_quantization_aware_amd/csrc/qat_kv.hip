@@ -830,15 +830,12 @@ __global__ __launch_bounds__(256, 2) void k_kv_prompt(const AttnArgs a) {
   __shared__ __attribute__((aligned(8))) uint16_t nan_at[2][D][4];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  // (row block, sequence and head): the blocks of one head on one XCD where the
-  // heads are a multiple of 8, the longest (last) blocks first
-  const int nrb = a.row_blocks, w = blockIdx.x;
-  int prob = w / nrb, rb = nrb - 1 - (w - prob * nrb);
-  if ((a.batch * a.hk & 7) == 0) {
-    const int r = w % (8 * nrb);
-    prob = 8 * (w / (8 * nrb)) + (r & 7);
-    rb = nrb - 1 - (r >> 3);
-  }
+  // (row block, sequence and head), the longest (last) row blocks of all heads
+  // first: in the order of heads, the last heads' long blocks began last, and a
+  // third of the time the chip was not full. Workgroups go to the 8 XCDs in
+  // turn, so a head stays on one where the heads are a multiple of 8.
+  const int probs = a.batch * a.hk, w = blockIdx.x;
+  const int rb = a.row_blocks - 1 - w / probs, prob = w % probs;
   const int b = prob / a.hk, h = prob - b * a.hk;
   const Seq s = seq_of(a, b);
   const int rows = s.n * a.group, row_base = rb * kRows;
@@ -1235,7 +1232,12 @@ constexpr int kTargetGroups = 256; // one workgroup for each CU: two measured th
 AttnPlan plan_attn(int64_t batch, int64_t hk, int64_t group, int d, int64_t max_new, int64_t max_len) {
   AttnPlan p;
   const int64_t rows = max_new * group;
-  p.prompt = rows > 32;
+  // Prompts' kernel or the other one by how many workgroups the first would have.
+  // It does not split a sequence, and a workgroup takes 1.7 us a block of
+  // positions however few there are (1 x 20 tokens over 8000, 8 key heads, 8
+  // workgroups: 217 us, the other kernel 20; 1 x 300 over 4000, 80: 114 and 60;
+  // 2 x 2048 over themselves, 1024: 92 and 170).
+  p.prompt = rows > 32 && batch * hk * ((rows + 127) / 128) * 4 >= 3 * kTargetGroups;
   if (p.prompt) {
     p.row_blocks = (int)((rows + 127) / 128);
     p.target = p.parts = 0;
