@@ -15,14 +15,15 @@
  * sequence b, cu[0] = 0. lens [batch] int32 is each sequence's length with
  * those tokens, so new token i of sequence b has position lens[b] - n_b + i,
  * n_b = cu[b + 1] - cu[b]. A sequence may have no new tokens, and no tokens at
- * all. max_new is a host-side bound on every n_b, max_len on every lens[b].
+ * all. max_new is a host-side bound on every n_b, max_len on every lens[b]; the
+ * kernels and their grids are chosen by them, so they should be near the truth.
  *
  * The cache: pages of `page` tokens (16, 32, 64 or 128).
  *   k_cache [n_pages][heads][page][head_dim] e4m3 (OCP FP8 E4M3, uint8)
  *   v_cache [n_pages][heads][head_dim][page] e4m3: a value block is stored
  *           with its tokens innermost, the order in which the matrix cores
  *           contract over them
- *   k_scale, v_scale [n_pages][heads] fp32: a value is code * scale
+ *   k_scale, v_scale [n_pages][heads] fp32, not negative: a value is code * scale
  *   table [batch][table_cols] int32: position p of sequence b is in slot
  *           p % page of page table[b][p / page].
  * The lengths, cu and table are read on the device and never trusted for an
@@ -84,8 +85,9 @@ int32_t qat_rope(const void* q, const void* k, const int32_t* pos, const float* 
  * are rounded again where e grew); infinities and NaN become the NaN code.
  * Slots of other positions keep their codes. Scales of blocks that hold
  * tokens are expected to be powers of two, as this call makes them. Left out
- * (not written): tokens that have no slot as said above. Two sequences must
- * not append to one page in the same call.
+ * (not written): tokens that have no slot as said above. No page may be
+ * appended to through two entries of the table in the same call (two sequences,
+ * or one twice): its contents are undefined then.
  */
 int32_t qat_kv_append(const void* k, const void* v, int32_t dtype, int64_t ldk, int64_t ldv, const int32_t* cu,
                       const int32_t* lens, const int32_t* table, int64_t table_cols, int64_t tokens, int64_t batch,

@@ -481,3 +481,68 @@ def test_workspace_too_small_is_refused():
         assert e.value.status == 6
     torch.cuda.synchronize()
     assert (out == 3).all()
+
+
+@pytest.mark.parametrize("new,hk", [(1, 2), (40, 96)])
+def test_attn_page_scales_that_are_not_numbers_or_zero(new, hk):
+    # a NaN scale of a page that is seen shows; zero scales give scores of zero and values of zero
+    n, d = 100, 64
+    q = rand((new, hk, d), 3, BF)
+    run = lambda c, o: Q.qat_kv_attn(q, i32([0, new]), i32([n]), c.tab(), *c.device(), o, 0.125,
+                                     ws=Q.workspace(1 << 24))
+    for what in ("ks", "vs"):
+        c = Cache([n], hk, d, 32).fill()
+        getattr(c, what)[c.table[0, 0]] = np.nan
+        o = torch.zeros_like(q)
+        run(c, o)
+        assert torch.isnan(o).all(), what
+    c = Cache([n], hk, d, 32).fill()
+    c.vs[c.table[0]] = 0
+    o = torch.ones_like(q)
+    run(c, o)
+    assert (o == 0).all()
+    c = Cache([n], hk, d, 32).fill()
+    c.ks[c.table[0, 1]] = 0
+    check_attn(c, q, [0, new], [n], 0.125, True)
+
+
+def test_decode_step_captured_and_replayed():
+    # rope, append and attention of three sequences as one graph; lengths and positions move on the device
+    hq, hk, d, page, start = 8, 2, 64, 16, [30, 5, 61]
+    c = Cache([l + 6 for l in start], hk, d, page).fill()
+    for b, l in enumerate(start):               # only the first `start` positions are there
+        for p in range(l, l + 6):
+            c.k[c.table[b, p // page], :, p % page] = 0x7F
+            c.v[c.table[b, p // page], :, p % page] = 0x7F
+    devs = [c.device(), c.device()]
+    cu, tab, f = i32([0, 1, 2, 3]), c.tab(), Q.rope_inv_freq(d)[0].cuda()
+    qkv = torch.empty(3, (hq + 2 * hk) * d, dtype=BF, device="cuda")
+    top = max(start) + 6
+    ws = Q.workspace(Q.kv_attn_ws_bytes(3, 3, hq, hk, d, 1, top))
+    lens, pos = i32(start), i32([l - 1 for l in start])
+
+    def step(dev, x, out):
+        q, k, v = (x[:, a * d:b * d].view(3, b - a, d) for a, b in ((0, hq), (hq, hq + hk), (hq + hk, hq + 2 * hk)))
+        Q.qat_rope(q, pos, f, q, k=k, k_out=k)
+        Q.qat_kv_append(k, v, cu, lens, tab, *dev, max_new=1)
+        Q.qat_kv_attn(q, cu, lens, tab, *dev, out, 0.125, max_new=1, max_len=top, ws=ws)
+
+    outs = [torch.empty(3, hq, d, dtype=BF, device="cuda") for _ in range(2)]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            step(devs[0], qkv, outs[0])
+    torch.cuda.current_stream().wait_stream(st)
+    for i in range(5):
+        x = rand(qkv.shape, 70 + i, BF)
+        lens.add_(1)
+        pos.add_(1)
+        qkv.copy_(x)
+        graph.replay()
+        step(devs[1], x, outs[1])
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], outs[1]) and torch.isfinite(outs[0].float()).all(), i
+        for a, b in zip(*devs):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i

@@ -137,6 +137,7 @@ GEMM = [
     # contractions, and several tiles for a workgroup
     (33, 4100, 4640), (333, 1031, 4640), (1030, 2100, 1056), (1500, 1900, 2080), (2100, 3001, 544), (2300, 3008, 1536),
     (4129, 4100, 288), (4096, 4864, 1056), (5000, 4099, 32),
+    (8200, 5700, 32), (1100000, 8, 32),
 ]
 
 
@@ -198,9 +199,8 @@ def test_linear_of_a_block_with_an_infinity():
     assert torch.isnan(y[1]).all() and torch.isfinite(y[::2]).all()
 
 
-@pytest.mark.parametrize("M", [1, 40, 300])
-def test_other_stream_and_replayed_graph(M):
-    N, K = 300, 1056
+@pytest.mark.parametrize("M,N,K", [(1, 300, 1056), (40, 300, 1056), (600, 3000, 2080)])
+def test_other_stream_and_replayed_graph(M, N, K):
     wc, ws, wv = operand(N, K, 10, 112, 122)
     work = Q.workspace(Q.mx_ws_bytes(M, N, K))
     x = torch.randn(M, K, device="cuda").half()

@@ -489,6 +489,22 @@ __device__ __forceinline__ bool has_nan(uint4 u) {
   return ((((u.x & k7) + k1) | ((u.y & k7) + k1) | ((u.z & k7) + k1) | ((u.w & k7) + k1)) & 0x80808080u) != 0;
 }
 
+// What a key page's scale and the softmax's make of a score, for a lane whose
+// positions hold `have` keys: positive, so that the maximum can be taken before
+// it, and never zero, so that a masked score stays -inf. A scale that is not a
+// number stays one; that of a page left out does not matter.
+__device__ __forceinline__ float score_factor(float key_scale, float scale_log2, int have) {
+  const float f = have > 0 ? key_scale * scale_log2 : 1.0f;
+  return f < 0x1p-126f ? 0x1p-126f : f;
+}
+
+// log2 of a value page's scale over the reference, at kLowC or more (also where
+// both are zero).
+__device__ __forceinline__ float scale_over(float lv, float vref, int have) {
+  const float d = lv - vref;
+  return have <= 0 ? 0.0f : lv != lv ? lv : d > kLowC ? d : kLowC;
+}
+
 // The first `n` (0 .. 16) bytes of 16, the others zero.
 __device__ __forceinline__ uint4 first_bytes(uint4 u, int n) {
   uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -628,9 +644,7 @@ __global__ __launch_bounds__(256, 2) void k_kv_decode(const AttnArgs a) {
           }
         }
         if (more) load_k(t + 4);
-        // positive, so that the maximum can be taken before it, and never zero, so
-        // that a masked score stays -inf
-        const float f = fmaxf(xks * a.scale_log2, 0x1p-126f);
+        const float f = score_factor(xks, a.scale_log2, have);
         const int key0 = 64 * t + 16 * g;
         float mx[RT];
         bool grow = false;
@@ -671,7 +685,7 @@ __global__ __launch_bounds__(256, 2) void k_kv_decode(const AttnArgs a) {
         }
         // w = 2^(s f + log2 c - m), c the lane's value scale over the reference; the
         // softmax's sum takes 1 / c once for the lane's 16 positions
-        const float lc = have > 0 ? fmaxf(lv - vref, kLowC) : 0.0f;
+        const float lc = scale_over(lv, vref, have);
         const float rc = __builtin_amdgcn_exp2f(-lc);
         f16x8 pf[RT][2];
 #pragma unroll
@@ -1005,9 +1019,7 @@ __global__ __launch_bounds__(256, 2) void k_kv_prompt(const AttnArgs a) {
           sc[i][jt] = mfma16(kf[jt & 1][ks], qf[i][ks], ks ? sc[i][jt] : f32x4{0.f, 0.f, 0.f, 0.f});
       __builtin_amdgcn_sched_barrier(0);
     }
-    // positive, so that the maximum can be taken before it, and never zero, so
-    // that a masked score stays -inf
-    const float f = fmaxf(kscale * a.scale_log2, 0x1p-126f);
+    const float f = score_factor(kscale, a.scale_log2, have);
     if (edge) {
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
@@ -1025,7 +1037,7 @@ __global__ __launch_bounds__(256, 2) void k_kv_prompt(const AttnArgs a) {
     // w = 2^(s f + log2 c - m), c the lane's value scale over the reference; the
     // softmax's sum takes 1 / c once for the lane's 16 positions
     auto weights = [&]() {
-      const float lc = have > 0 ? fmaxf(lv - vref, kLowC) : 0.0f;
+      const float lc = scale_over(lv, vref, have);
       rc = __builtin_amdgcn_exp2f(-lc);
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
@@ -1470,6 +1482,7 @@ QAT_API int32_t qat_kv_attn(const void* q, int32_t dtype, int64_t ldq, const int
   if (heads_q <= 0 || heads_q > 4096 || heads_q % heads_kv || max_len < 0 || max_len > kMaxCount ||
       !(softmax_scale > 0) || !(softmax_scale < INFINITY))
     return QAT_ERR_SHAPE;
+  if ((max_new < tokens ? max_new : tokens) * (heads_q / heads_kv) > kMaxCount) return QAT_ERR_SHAPE;
   const int64_t row = (int64_t)heads_q * head_dim, krow = (int64_t)heads_kv * head_dim;
   QAT_CHECK(check_ld(ldq, row));
   QAT_CHECK(check_ld(ldo, row));

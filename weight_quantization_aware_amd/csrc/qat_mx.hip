@@ -710,6 +710,7 @@ int num_cus() {
 // 4096 and more (32 x 4096 x 4096: 6 us against 14; 32 x 11008 x 4096: 15
 // against 15; 128 x 4096 x 4096: 20 against 14).
 bool tiled(int64_t M, int64_t out, int64_t in) {
+  if ((M + 15) / 16 > 65535) return true;                 // the other one's grid
   return M > 16 && (M + 15) / 16 * ((out + 15) / 16) * in > (int64_t(11) << 19);
 }
 
