@@ -457,18 +457,35 @@ class _RowArgs(_Args):
     there is one.
     """
 
-    def t(self, name: str, t, dtypes, shape=None, optional: bool = False, min_bytes: Optional[int] = None):
-        if isinstance(t, torch.Tensor) and (dtypes is None or t.dtype in dtypes) and min_bytes is None and (
-                shape is None or t.shape == shape) and t.is_contiguous():
+    def __init__(self, fn: str):
+        super().__init__(fn)
+        self.dev = None              # of the first tensor (-1: not on a GPU)
+        self.other = None            # a tensor on another one, told once all types and shapes are checked
+
+    def t(self, name: str, t, dtypes, shape=None, optional: bool = False):
+        try:
+            ok = (dtypes is None or t.dtype in dtypes) and (shape is None or t.shape == shape) and t.is_contiguous()
+        except AttributeError:
+            ok = False
+        if not ok and super().t(name, t, dtypes, shape, optional) is None:      # says what is wrong
+            return None
+        if t.get_device() != self.dev:
+            self._device(name, t)
+        return t.data_ptr()
+
+    def _device(self, name: str, t) -> None:
+        if self.dev is None:
+            self.dev = t.get_device()
             self.seen.append((name, t))
-            return t.data_ptr()
-        return super().t(name, t, dtypes, shape, optional, min_bytes)
+        else:
+            self.other = (name, t)
 
     def rows(self, name: str, t, dtypes, shape):
         """(pointer, elements between rows) of a tensor [rows, ...] whose trailing dimensions are contiguous."""
         if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape:
             super().t(name, t, dtypes, shape)                # says what is wrong
-        self.seen.append((name, t))
+        if t.get_device() != self.dev:
+            self._device(name, t)
         if t.is_contiguous():
             return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(math.prod(shape[1:]), 1)
         row = math.prod(shape[1:])
@@ -483,10 +500,11 @@ class _RowArgs(_Args):
         return t.data_ptr(), ld
 
     def call(self, *args) -> None:
-        dev = self.seen[0][1].get_device()
-        for _, t in self.seen:
-            if t.get_device() != dev or dev < 0:
-                self.done()                                  # says what is wrong
+        dev = self.dev
+        if self.other is not None or dev < 0:
+            if self.other is not None:
+                self.seen.append(self.other)
+            self.done()                                      # says what is wrong
         if dev == _current_device():
             _call(self.fn, *args, _raw_stream(dev))
         else:
