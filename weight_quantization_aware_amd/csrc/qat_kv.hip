@@ -1252,8 +1252,8 @@ AttnPlan plan_attn(int64_t batch, int64_t hk, int64_t group, int d, int64_t max_
   // Prompts' kernel or the other one by how many workgroups the first would have.
   // It does not split a sequence, and a workgroup takes 1.7 us a block of
   // positions however few there are (1 x 20 tokens over 8000, 8 key heads, 8
-  // workgroups: 217 us, the other kernel 20; 1 x 300 over 4000, 80: 114 and 60;
-  // 2 x 2048 over themselves, 1024: 92 and 170).
+  // workgroups: 217 us, the other kernel 27; 1 x 300 over 4000, 80: 114 and 70;
+  // 1 x 700 over 2000, 176: 61 and 66; 2 x 2048 over themselves, 1024: 92 and 170).
   p.prompt = rows > 32 && batch * hk * ((rows + 127) / 128) * 4 >= 3 * kTargetGroups;
   if (p.prompt) {
     p.row_blocks = (int)((rows + 127) / 128);
